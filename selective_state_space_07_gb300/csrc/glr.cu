@@ -36,13 +36,16 @@
 // in fp32 from the states that the forward saved every 32 tokens, so no bf16
 // copy of them enters the gradients.
 //
-// Measured, bf16 unless said, in percent of the HBM copy rate: 4 x 4096 x 4096
-// forward with checkpoints 102 us (77%), backward 203 (68%); 4 x 2048 x 4096
-// fp32 89 (88%) and 158 (88%). There the instructions bound it, 32 an element
-// and 59, at half of the issue slots. 1 x 65536 x 2048: 265 us (60%) and 512;
-// each of its 19 chunks at work at a time waits for those before it. 2 x 509 x 256
-// fp32, both passes 22 us: launches.
+// Measured, bf16 unless said, in percent of the HBM copy rate, for slow decays
+// (c softplus(lam) < 1/4): 4 x 4096 x 4096 forward with checkpoints 101 us
+// (79%), backward 208 (67%), other decays 108 and 230; 4 x 2048 x 4096 fp32 89
+// (88%) and 161 (86%). 1 x 65536 x 2048: 267 us (59%) and 520, other decays 281
+// and 600; each of its 19 chunks at work at a time waits for those before it.
+// Registers allow 16 warps an SM forward and 12 backward, which issue in half
+// of the slots (32 and 59 instructions an element). 2 x 509 x 256 fp32, both
+// passes 22 us: launches.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/glr.h"
 #include "ssm_common.cuh"
@@ -178,30 +181,55 @@ template <> struct Pair<__nv_bfloat16> {
 
 __device__ __forceinline__ float softplus_full(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
 
-// The gates of two channels, cs = c * softplus(lam): t = cs r = -log a and
-// w = 1 - a, from which a = 1 - w and 1 - a^2 = w (2 - w) follow without
-// cancelling for decays near 1, where w has all its digits and a rounds
-// freshly. Below t = 1/4, w = t (1 - t/2 + t^2/6 - ...), the terms left out
-// below 5e-8 of the sum; above, w = 1 - 2^(-t log2e).
+// The gates of two channels, cs = c * softplus(lam): of t = cs r = -log a come
+// a = exp(-t) and w = 1 - a, each with all its digits, so that neither slow
+// decays (w, and 1 - a^2 = w (2 - w)) nor fast ones (a) cancel. Below t = 1/4,
+// w = t (1 - t/2 + t^2/6 - ...), the terms left out below 5e-8 of the sum, and
+// a = 1 - w; above, a = 2^(-t log2e) and w = 1 - a.
 // exp and reciprocal are the MUFU forms for both I/O types: their relative
 // errors (2^-22) are those of fp32 sums.
 // SERIES: every t of the warp is known to be below 1/4 (t = cs r <= cs).
-template <bool SERIES> __device__ __forceinline__ float2 one_minus_decay(float2 t) {
+struct Decay {
+    float2 a, w;
+};
+__device__ __forceinline__ float2 one_minus(float2 v) { return __ffma2_rn(v, dup(-1.f), dup(1.f)); }
+template <bool SERIES> __device__ __forceinline__ Decay decay(float2 t) {
     float2 p = __ffma2_rn(t, dup(-1.0f / 720), dup(1.0f / 120));
     p = __ffma2_rn(p, t, dup(-1.0f / 24));
     p = __ffma2_rn(p, t, dup(1.0f / 6));
     p = __ffma2_rn(p, t, dup(-0.5f));
     p = __ffma2_rn(p, t, dup(1.0f));
     p = __fmul2_rn(p, t);
-    if (SERIES) return p;
-    const float2 e = __fmul2_rn(t, dup(-kLog2e));
-    return pk(t.x < 0.25f ? p.x : 1.0f - ex2(e.x), t.y < 0.25f ? p.y : 1.0f - ex2(e.y));
+    const float2 q = one_minus(p);
+    if (SERIES) return {q, p};
+    const float2 z = __fmul2_rn(t, dup(-kLog2e)), e = pk(ex2(z.x), ex2(z.y)), f = one_minus(e);
+    return {pk(t.x < 0.25f ? q.x : e.x, t.y < 0.25f ? q.y : e.y), pk(t.x < 0.25f ? p.x : f.x, t.y < 0.25f ? p.y : f.y)};
 }
-// Whether the series is enough for all of a warp's channels. (It alone: 102 us
-// forward, 203 backward at 4 x 4096 x 4096 bf16; with the choice for each
-// element 106 and 250.)
+// Both in one word, for the backward, which keeps them for each token: v = w
+// near 1, else v = -a (never -0). With n = 1 where v >= 0 and 0 elsewhere,
+// a = n - v and 1 - a^2 = v (a + n) + 1 - n.
+template <bool SERIES> __device__ __forceinline__ float2 hold(const Decay& d) {
+    if (SERIES) return d.w;
+    const float2 v = __ffma2_rn(d.a, dup(-1.f), dup(-1.17549435e-38f));
+    return pk(d.w.x < 0.2211f ? d.w.x : v.x, d.w.y < 0.2211f ? d.w.y : v.y);
+}
+__device__ __forceinline__ float not_negative(float v) {
+    float n;
+    asm("set.ge.f32.f32 %0, %1, 0f00000000;" : "=f"(n) : "f"(v));
+    return n;
+}
+struct Held {
+    float2 n, a;
+};
+template <bool SERIES> __device__ __forceinline__ Held held_decay(float2 v) {
+    if (SERIES) return {dup(1.f), one_minus(v)};
+    const float2 n = pk(not_negative(v.x), not_negative(v.y));
+    return {n, __ffma2_rn(v, dup(-1.f), n)};
+}
+// Whether the series is enough for all of a warp's channels. (It alone: 101 us
+// forward, 208 backward at 4 x 4096 x 4096 bf16; with the choice for each
+// element 108 and 230.)
 __device__ __forceinline__ bool all_series(float2 cs) { return __all_sync(0xffffffffu, cs.x < 0.25f && cs.y < 0.25f); }
-__device__ __forceinline__ float2 one_minus(float2 v) { return __ffma2_rn(v, dup(-1.f), dup(1.f)); }
 // 1 - a^2 of w = 1 - a
 __device__ __forceinline__ float2 input_power(float2 w) { return __fmul2_rn(w, __ffma2_rn(w, dup(-1.f), dup(2.f))); }
 __device__ __forceinline__ float2 sqrt2(float2 v) { return pk(sqrt_approx(v.x), sqrt_approx(v.y)); }
@@ -378,10 +406,9 @@ __device__ __forceinline__ float4 run_forward(float2 cs, Load load, float2 (&h)[
     for (int j = 0; j < kTok<IO>; ++j) {
         float2 x, rg, ig;
         load(j, x, rg, ig);
-        const float2 w = one_minus_decay<SERIES>(__fmul2_rn(cs, sigmoid2<true>(rg)));
-        const float2 a = one_minus(w);
-        hh = __ffma2_rn(a, hh, __fmul2_rn(__fmul2_rn(sqrt2(input_power(w)), sigmoid2<true>(ig)), x));
-        pp = __fmul2_rn(pp, a);
+        const Decay d = decay<SERIES>(__fmul2_rn(cs, sigmoid2<true>(rg)));
+        hh = __ffma2_rn(d.a, hh, __fmul2_rn(__fmul2_rn(sqrt2(input_power(d.w)), sigmoid2<true>(ig)), x));
+        pp = __fmul2_rn(pp, d.a);
         h[j] = hh;
         pr[j] = pp;
     }
@@ -414,8 +441,9 @@ __device__ __forceinline__ float finish_forward(const GlrParams& p, const Tile& 
     return __fmaf_rn(y.x, 0.f, y.y * 0.f);
 }
 
-// The warp's run in the backward, before the carries are known: w = 1 - a and
-// the gates (kept), the run's map (P, H) forwards and V backwards.
+// The warp's run in the backward, before the carries are known: the decays (w,
+// held in one word each) and the gates (kept; the input gates in the series
+// only), the run's map (P, H) forwards and V backwards.
 template <typename IO, bool SERIES, typename Load>
 __device__ __forceinline__ float4 run_backward(float2 cs, Load load, float2 (&w)[kTok<IO>], float2 (&r)[kTok<IO>],
                                                float2 (&i)[kTok<IO>], float2& back) {
@@ -425,11 +453,12 @@ __device__ __forceinline__ float4 run_backward(float2 cs, Load load, float2 (&w)
         float2 x, rg, ig, dy;
         load(j, x, rg, ig, dy);
         r[j] = sigmoid2<true>(rg);
-        i[j] = sigmoid2<true>(ig);
-        w[j] = one_minus_decay<SERIES>(__fmul2_rn(cs, r[j]));
-        const float2 a = one_minus(w[j]);
-        hh = __ffma2_rn(a, hh, __fmul2_rn(__fmul2_rn(sqrt2(input_power(w[j])), i[j]), x));
-        pp = __fmul2_rn(pp, a);
+        const float2 iv = sigmoid2<true>(ig);
+        if (SERIES) i[j] = iv;
+        const Decay d = decay<SERIES>(__fmul2_rn(cs, r[j]));
+        w[j] = hold<SERIES>(d);
+        hh = __ffma2_rn(d.a, hh, __fmul2_rn(__fmul2_rn(sqrt2(input_power(d.w)), iv), x));
+        pp = __fmul2_rn(pp, d.a);
         vv = __ffma2_rn(pp, dy, vv);  // V = sum_j (a_0 ... a_j) dy_j
     }
     back = vv;
@@ -439,17 +468,17 @@ __device__ __forceinline__ float4 run_backward(float2 cs, Load load, float2 (&w)
 // comes in from behind it are known. Returns what its first token hands on;
 // `sum` is the run's sum of dloga * r, which is not finite where a gradient
 // or a state is not.
-template <typename IO, typename Load>
+template <typename IO, bool SERIES, typename Load>
 __device__ __forceinline__ float2 finish_backward(const GlrParams& p, const Tile& t, const Lane<IO>& at, float2 cs, float2 h, float2 v,
                                                   Load load, const float2 (&w)[kTok<IO>], const float2 (&r)[kTok<IO>],
                                                   const float2 (&i)[kTok<IO>], float2& sum) {
     float2 g[kTok<IO>];
 #pragma unroll
     for (int j = kTok<IO> - 1; j >= 0; --j) {
-        float2 x, dy;
-        load(j, x, dy);
+        float2 x, ig, dy;
+        load(j, x, ig, dy);
         g[j] = __fadd2_rn(dy, v);
-        v = __fmul2_rn(one_minus(w[j]), g[j]);
+        v = __fmul2_rn(held_decay<SERIES>(w[j]).a, g[j]);
     }
     const float2 ncs = pk(-cs.x, -cs.y);
     const unsigned D = (unsigned)p.D;
@@ -459,14 +488,18 @@ __device__ __forceinline__ float2 finish_backward(const GlrParams& p, const Tile
     sum = dup(0.f);
 #pragma unroll
     for (int j = 0; j < kTok<IO>; ++j) {
-        float2 x, dy;
-        load(j, x, dy);
-        const float2 a = one_minus(w[j]), m2 = input_power(w[j]);
+        float2 x, ig, dy;
+        load(j, x, ig, dy);
+        const float2 iv = SERIES ? i[j] : sigmoid2<true>(ig);
+        float2 wj = w[j];
+        asm volatile("" : "+f"(wj.x), "+f"(wj.y));  // (a is taken from it again: kept from above it would cost registers)
+        const Held d = held_decay<SERIES>(wj);
+        const float2 a = d.a, m2 = SERIES ? input_power(wj) : __ffma2_rn(wj, __fadd2_rn(a, d.n), one_minus(d.n));
         // 1/m; where a = 1 the floor keeps it finite, and r or cs makes the product below 0
         const float2 inv = pk(rsqrt_approx(fmaxf(m2.x, 1e-36f)), rsqrt_approx(fmaxf(m2.y, 1e-36f)));
-        const float2 ix = __fmul2_rn(i[j], x), m = __fmul2_rn(m2, inv);
-        const float2 dx = __fmul2_rn(g[j], __fmul2_rn(m, i[j]));
-        const float2 di = __fmul2_rn(__fmul2_rn(dx, x), one_minus(i[j]));
+        const float2 ix = __fmul2_rn(iv, x), m = __fmul2_rn(m2, inv);
+        const float2 dx = __fmul2_rn(g[j], __fmul2_rn(m, iv));
+        const float2 di = __fmul2_rn(__fmul2_rn(dx, x), one_minus(iv));
         const float2 ah = __fmul2_rn(a, h);
         const float2 nai = __fmul2_rn(__fmul2_rn(a, inv), __fmul2_rn(a, dup(-1.f)));  // -a^2/m
         const float2 dlr = __fmul2_rn(__fmul2_rn(g[j], __ffma2_rn(nai, ix, ah)), r[j]);
@@ -563,7 +596,8 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) glr_bwd_short
         const float4 f = maps.run[u][lane];
         v = __ffma2_rn(pk(f.x, f.y), v, maps.back[u][lane]);
     }
-    v = finish_backward<IO>(p, t, at, cs, h, v, [&](int j, float2& xv, float2& gv) { xv = x.f(j), gv = dy.f(j); }, w, r, i, sum);
+    v = finish_backward<IO, false>(
+        p, t, at, cs, h, v, [&](int j, float2& xv, float2& iv, float2& gv) { xv = x.f(j), iv = ig.f(j), gv = dy.f(j); }, w, r, i, sum);
     if (p.end && warp == 0 && live) *reinterpret_cast<float2*>(p.end + t.state + at.ch) = v;
     flag_nonfinite(p.status, live ? (sum.x + sum.y + v.x + v.y) * 0.f : 0.f);
     red[warp][lane] = sum;
@@ -756,51 +790,58 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) glr_bwd_kernel(const GlrPa
             x = Pair<IO>::f(Pair<IO>::lds(q + 2 * kBoxBytes<IO>));
             dy = Pair<IO>::f(Pair<IO>::lds(q + 3 * kBoxBytes<IO>));
         };
-        float2 w[T], r[T], i[T], back, sum;
-        const float4 mine = all_series(cs) ? run_backward<IO, true>(cs, load, w, r, i, back)
-                                           : run_backward<IO, false>(cs, load, w, r, i, back);
-        run.run[warp][lane] = mine;
-        run.back[warp][lane] = back;
-        __syncthreads();
-        const bool failed = look.failed;
-        // the tile's tokens behind the warp's, composed from the last one on, and the state before the warp's
-        float4 behind = kIdentity;
-#pragma unroll
-        for (int u = kWarps - 1; u > 0; --u) {
-            if (u > warp) {
-                const float4 f = run.run[u][lane];
-                const float2 v = run.back[u][lane];
-                behind = compose(behind, make_float4(f.x, f.y, v.x, v.y));
-            }
-        }
-        const float4 whole = compose(behind, make_float4(mine.x, mine.y, back.x, back.y));  // warp 0: the tile's map
-        if (warp == 0) publish_map(p, t, whole);
-#pragma unroll
-        for (int u = 0; u < kWarps - 1; ++u)
-            if (u < warp) h = apply(run.run[u][lane], h);
-        if (!failed) look_chunks(p, look, t.k, t.col);
-        if (SPAN > kBlock && closes(p, t.k, kBlock)) {
+        float2 sum;
+        // A body for each way to the decays (the warps of a CTA have the same channels, and so take the same one): with
+        // one for both, or with the input gates kept outside the series too, registers spill (4 x 4096 x 4096 bf16:
+        // 208 us in the series and 230 outside, otherwise 250 to 320).
+        auto work = [&](auto way) {
+            constexpr bool SERIES = decltype(way)::value;
+            float2 w[T], r[T], i[T], back;
+            const float4 mine = run_backward<IO, SERIES>(cs, load, w, r, i, back);
+            run.run[warp][lane] = mine;
+            run.back[warp][lane] = back;
             __syncthreads();
-            if (warp == 0) publish_block(p, look, t, whole);
-        }
-        if (!failed) look_blocks<SPAN>(p, look, t.k, t.col, p.start && live ? p.start + t.state + at.ch : nullptr);
-        __syncthreads();
-        if (look.failed) {
-            drain<ST>(ring, it, it + ST - 1, total);
-            return;
-        }
-        const float2 carry = look_carry<SPAN>(look, t.k);
-        if (warp == 0 && closes(p, t.k, SPAN)) publish_state<SPAN>(p, t, apply(whole, carry));
-        const float2 v = finish_backward<IO>(
-            p, t, at, cs, h, apply(behind, carry),
-            [&](int j, float2& x, float2& dy) {
+            const bool failed = look.failed;
+            // the tile's tokens behind the warp's, composed from the last one on, and the state before the warp's
+            float4 behind = kIdentity;
+#pragma unroll
+            for (int u = kWarps - 1; u > 0; --u) {
+                if (u > warp) {
+                    const float4 f = run.run[u][lane];
+                    const float2 v = run.back[u][lane];
+                    behind = compose(behind, make_float4(f.x, f.y, v.x, v.y));
+                }
+            }
+            const float4 whole = compose(behind, make_float4(mine.x, mine.y, back.x, back.y));  // warp 0: the tile's map
+            if (warp == 0) publish_map(p, t, whole);
+#pragma unroll
+            for (int u = 0; u < kWarps - 1; ++u)
+                if (u < warp) h = apply(run.run[u][lane], h);
+            if (!failed) look_chunks(p, look, t.k, t.col);
+            if (SPAN > kBlock && closes(p, t.k, kBlock)) {
+                __syncthreads();
+                if (warp == 0) publish_block(p, look, t, whole);
+            }
+            if (!failed) look_blocks<SPAN>(p, look, t.k, t.col, p.start && live ? p.start + t.state + at.ch : nullptr);
+            __syncthreads();
+            if (look.failed) {
+                drain<ST>(ring, it, it + ST - 1, total);
+                return false;
+            }
+            const float2 carry = look_carry<SPAN>(look, t.k);
+            if (warp == 0 && closes(p, t.k, SPAN)) publish_state<SPAN>(p, t, apply(whole, carry));
+            const auto again = [&](int j, float2& x, float2& ig, float2& dy) {
                 const char* q = in + j * kCols * sizeof(IO);
+                ig = Pair<IO>::f(Pair<IO>::lds(q + kBoxBytes<IO>));
                 x = Pair<IO>::f(Pair<IO>::lds(q + 2 * kBoxBytes<IO>));
                 dy = Pair<IO>::f(Pair<IO>::lds(q + 3 * kBoxBytes<IO>));
-            },
-            w, r, i, sum);
-        acc += live ? (sum.x + sum.y + v.x + v.y) * 0.f : 0.f;
-        if (p.end && t.chunk == 0 && warp == 0 && live) *reinterpret_cast<float2*>(p.end + t.state + at.ch) = v;
+            };
+            const float2 v = finish_backward<IO, SERIES>(p, t, at, cs, h, apply(behind, carry), again, w, r, i, sum);
+            acc += live ? (sum.x + sum.y + v.x + v.y) * 0.f : 0.f;
+            if (p.end && t.chunk == 0 && warp == 0 && live) *reinterpret_cast<float2*>(p.end + t.state + at.ch) = v;
+            return true;
+        };
+        if (!(all_series(cs) ? work(std::true_type{}) : work(std::false_type{}))) return;
         red[warp][lane] = sum;
         __syncthreads();
         if (threadIdx.x == 0) {  // the stage has been read for the last time: its next tile
@@ -864,9 +905,9 @@ __global__ void __launch_bounds__(128) glr_step_kernel(int64_t B, int64_t D, int
         float2* hp = reinterpret_cast<float2*>(state + b * D + d);
         const float2 h0 = *hp, lv = __ldg(reinterpret_cast<const float2*>(lam + d));
         const float2 cs = pk(c * softplus_full(lv.x), c * softplus_full(lv.y));
-        const float2 w = one_minus_decay<false>(__fmul2_rn(cs, sigmoid2<true>(rv)));
-        const float2 u = __fmul2_rn(__fmul2_rn(sqrt2(input_power(w)), sigmoid2<true>(iv)), xv);
-        const float2 h = __ffma2_rn(one_minus(w), h0, u);
+        const Decay f = decay<false>(__fmul2_rn(cs, sigmoid2<true>(rv)));
+        const float2 u = __fmul2_rn(__fmul2_rn(sqrt2(input_power(f.w)), sigmoid2<true>(iv)), xv);
+        const float2 h = __ffma2_rn(f.a, h0, u);
         *hp = h;
         st2<IO>(y + b * D + d, h);
         acc = __fmaf_rn(h.x, 0.f, h.y * 0.f);
