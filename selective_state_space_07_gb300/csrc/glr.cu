@@ -38,8 +38,8 @@
 //
 // Measured, bf16 unless said, in percent of the HBM copy rate, for slow decays
 // (c softplus(lam) < 1/4): 4 x 4096 x 4096 forward with checkpoints 101 us
-// (79%), backward 208 (67%), other decays 108 and 230; 4 x 2048 x 4096 fp32 89
-// (88%) and 161 (86%). 1 x 65536 x 2048: 267 us (59%) and 520, other decays 281
+// (79%), backward 208 (67%), other decays 108 and 230; 4 x 2048 x 4096 fp32 90
+// (87%) and 159 (87%). 1 x 65536 x 2048: 267 us (59%) and 520, other decays 281
 // and 600; each of its 19 chunks at work at a time waits for those before it.
 // Registers allow 16 warps an SM forward and 12 backward, which issue in half
 // of the slots (32 and 59 instructions an element). 2 x 509 x 256 fp32, both
@@ -186,9 +186,29 @@ __device__ __forceinline__ float softplus_full(float v) { return fmaxf(v, 0.0f) 
 // decays (w, and 1 - a^2 = w (2 - w)) nor fast ones (a) cancel. Below t = 1/4,
 // w = t (1 - t/2 + t^2/6 - ...), the terms left out below 5e-8 of the sum, and
 // a = 1 - w; above, a = 2^(-t log2e) and w = 1 - a.
-// exp and reciprocal are the MUFU forms for both I/O types: their relative
-// errors (2^-22) are those of fp32 sums.
+// The exponential of -t is the MUFU form for both I/O types: its relative error
+// (2^-22, and as much as t's own rounding) is that of fp32 sums. The sigmoid's
+// would grow with |z|, as n = -z log2e is rounded (6e-7 at z = -10, 4e-6 at
+// -70): in fp32 I/O its e = 2^n gets what n lacks (Cody and Waite's reduction),
+// e + e (-z - n ln 2). (4 x 2048 x 4096 fp32 with expf and divisions instead:
+// forward 118 us, backward 187 to 226.)
 // SERIES: every t of the warp is known to be below 1/4 (t = cs r <= cs).
+template <typename IO> __device__ __forceinline__ float2 gate2(float2 z) { return sigmoid2<true>(z); }
+__device__ __forceinline__ float within(float v, float most) {  // (a NaN stays one)
+    float u;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(u) : "f"(v), "f"(-most));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(u) : "f"(u), "f"(most));
+    return u;
+}
+template <> __device__ __forceinline__ float2 gate2<float>(float2 z) {
+    const float2 x = pk(within(-z.x, 88.0f), within(-z.y, 88.0f));  // (e^88 is finite, and its reciprocal flushed to 0)
+    const float2 n = __fmul2_rn(x, dup(kLog2e));
+    const float2 d = __ffma2_rn(n, dup(1.904654290e-9f), __ffma2_rn(n, dup(-kLn2), x));  // x - n ln 2, with ln 2 in two parts
+    float2 e = pk(ex2(n.x), ex2(n.y));
+    e = __ffma2_rn(e, d, e);
+    const float2 w = __fadd2_rn(dup(1.0f), e);
+    return pk(rcp(w.x), rcp(w.y));
+}
 struct Decay {
     float2 a, w;
 };
@@ -406,8 +426,8 @@ __device__ __forceinline__ float4 run_forward(float2 cs, Load load, float2 (&h)[
     for (int j = 0; j < kTok<IO>; ++j) {
         float2 x, rg, ig;
         load(j, x, rg, ig);
-        const Decay d = decay<SERIES>(__fmul2_rn(cs, sigmoid2<true>(rg)));
-        hh = __ffma2_rn(d.a, hh, __fmul2_rn(__fmul2_rn(sqrt2(input_power(d.w)), sigmoid2<true>(ig)), x));
+        const Decay d = decay<SERIES>(__fmul2_rn(cs, gate2<IO>(rg)));
+        hh = __ffma2_rn(d.a, hh, __fmul2_rn(__fmul2_rn(sqrt2(input_power(d.w)), gate2<IO>(ig)), x));
         pp = __fmul2_rn(pp, d.a);
         h[j] = hh;
         pr[j] = pp;
@@ -452,8 +472,8 @@ __device__ __forceinline__ float4 run_backward(float2 cs, Load load, float2 (&w)
     for (int j = 0; j < kTok<IO>; ++j) {
         float2 x, rg, ig, dy;
         load(j, x, rg, ig, dy);
-        r[j] = sigmoid2<true>(rg);
-        const float2 iv = sigmoid2<true>(ig);
+        r[j] = gate2<IO>(rg);
+        const float2 iv = gate2<IO>(ig);
         if (SERIES) i[j] = iv;
         const Decay d = decay<SERIES>(__fmul2_rn(cs, r[j]));
         w[j] = hold<SERIES>(d);
@@ -490,7 +510,7 @@ __device__ __forceinline__ float2 finish_backward(const GlrParams& p, const Tile
     for (int j = 0; j < kTok<IO>; ++j) {
         float2 x, ig, dy;
         load(j, x, ig, dy);
-        const float2 iv = SERIES ? i[j] : sigmoid2<true>(ig);
+        const float2 iv = SERIES ? i[j] : gate2<IO>(ig);
         float2 wj = w[j];
         asm volatile("" : "+f"(wj.x), "+f"(wj.y));  // (a is taken from it again: kept from above it would cost registers)
         const Held d = held_decay<SERIES>(wj);
@@ -905,8 +925,8 @@ __global__ void __launch_bounds__(128) glr_step_kernel(int64_t B, int64_t D, int
         float2* hp = reinterpret_cast<float2*>(state + b * D + d);
         const float2 h0 = *hp, lv = __ldg(reinterpret_cast<const float2*>(lam + d));
         const float2 cs = pk(c * softplus_full(lv.x), c * softplus_full(lv.y));
-        const Decay f = decay<false>(__fmul2_rn(cs, sigmoid2<true>(rv)));
-        const float2 u = __fmul2_rn(__fmul2_rn(sqrt2(input_power(f.w)), sigmoid2<true>(iv)), xv);
+        const Decay f = decay<false>(__fmul2_rn(cs, gate2<IO>(rv)));
+        const float2 u = __fmul2_rn(__fmul2_rn(sqrt2(input_power(f.w)), gate2<IO>(iv)), xv);
         const float2 h = __ffma2_rn(f.a, h0, u);
         *hp = h;
         st2<IO>(y + b * D + d, h);

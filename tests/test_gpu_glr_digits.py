@@ -129,3 +129,30 @@ def test_step_with_fast_decays(ssm):
     ref = np.exp(-tt) * h0
     rel = np.abs(y.cpu().numpy()[0] - ref) / ref
     assert torch.equal(y, state) and (rel < tt * 36 * U + 6 * U).all(), rel
+
+
+def nearly_closed(which, seed):
+    """One sort of gates spread over -70 .. -10, where a sigmoid is exp(z), the other as usual."""
+    a = inputs(2, 40, [0.1, 0.5, 2.0, 6.0, 0.1, 0.5, 2.0, 6.0], seed=seed)
+    z = -10 - 60 * gen.uniform53(seed, a[0].size).reshape(a[0].shape)
+    a[1 if which == "rgate" else 2] = z.astype(np.float32)
+    return a
+
+
+@pytest.mark.parametrize("which", ["rgate", "igate"])
+def test_nearly_closed_gates_keep_their_digits(ssm, which):
+    # of fp32 calls: as with expf (2 ulp at most), a sum and a division
+    a = nearly_closed(which, 31)
+    off = worst(on_gpu(ssm, *a), reference(*a), bounds(*a, d_s=6 * U))
+    assert max(off.values()) < 1, off
+
+
+def test_step_with_nearly_closed_gates(ssm):
+    x, _, ig, _, lam, _ = nearly_closed("igate", 32)
+    x, ig, lam = x.reshape(-1, 8), ig.reshape(-1, 8), lam_of([0.5] * 8)
+    t = lambda v: torch.from_numpy(np.ascontiguousarray(v, np.float32)).cuda()  # noqa: E731
+    state = torch.zeros(x.shape, device="cuda")
+    y = ssm.glr_step(state, t(x), t(np.full_like(x, 2.0)), t(ig), t(lam), c=C).cpu().numpy()
+    ref = np.sqrt(-np.expm1(-2 * C * G.softplus(lam.astype(np.float64)) * G.sigmoid(2.0))) * G.sigmoid(ig.astype(np.float64)) * x
+    # m's error: dw / 2 + 5 u with dw = (a (t (11 + 6 + 2 u) + 4 u) + u) / w below 20 u at t = 0.44; then i, and two products
+    assert (np.abs(y - ref) < (15 + 6 + 2) * U * np.abs(ref)).all(), np.max(np.abs(y / ref - 1)) / U
