@@ -94,6 +94,12 @@ struct Call {
         if ((uintptr_t)p & 15) return fail();
         return p;
     }
+    // A switch, as Python takes it: any object that counts as true.
+    bool flag(PyObject* o) {
+        const int v = o == Py_True ? 1 : o == Py_False ? 0 : PyObject_IsTrue(o);
+        if (v < 0) good = false;  // (it has no truth: the long way raises what it raised)
+        return v > 0;
+    }
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type) {
         return at::detail::empty_cuda(shape, type, device, std::nullopt);
     }
@@ -206,9 +212,9 @@ BINDING(glr_fwd, 13) {
     at::Tensor y, last, ckpt, scratch;
     s.h0 = call.dense<float>(a[5], at::kFloat, {s.B, s.D}, 16, true);
     s.y = call.out(a[6], y, x->scalar_type(), x->sizes(), 16);
-    if (a[7] != Py_None || a[9] == Py_True) s.h_last = call.out<float>(a[7], last, at::kFloat, {s.B, s.D}, 16);
+    if (a[7] != Py_None || call.flag(a[9])) s.h_last = call.out<float>(a[7], last, at::kFloat, {s.B, s.D}, 16);
     if (a[8] != Py_None) return none();  // (a buffer of the caller's may have any shape)
-    if (a[10] == Py_True) s.ckpt = call.out<float>(Py_None, ckpt, at::kFloat, {s.B, (s.L + kSavedEvery - 1) / kSavedEvery, s.D}, 16);
+    if (call.flag(a[10])) s.ckpt = call.out<float>(Py_None, ckpt, at::kFloat, {s.B, (s.L + kSavedEvery - 1) / kSavedEvery, s.D}, 16);
     if (!call.good || !glr_space(call, a[11], a[12], s, scratch) || lib.glr_fwd(&s, call.stream)) return none();
     return give({&y, &last, &ckpt});
 }
@@ -231,8 +237,8 @@ BINDING(glr_bwd, 11) {
     s.drgate = call.out(Py_None, dr, type, shape, 16);
     s.digate = call.out(Py_None, di, type, shape, 16);
     s.dlam = call.out<float>(Py_None, dlam, at::kFloat, {f.D}, 16);
-    if (a[8] == Py_True) s.dh0 = call.out<float>(Py_None, dh0, at::kFloat, {f.B, f.D}, 16);
-    if (!glr_space(call, a[9], a[10], s.f, scratch) || lib.glr_bwd(&s, call.stream)) return none();
+    if (call.flag(a[8])) s.dh0 = call.out<float>(Py_None, dh0, at::kFloat, {f.B, f.D}, 16);
+    if (!call.good || !glr_space(call, a[9], a[10], s.f, scratch) || lib.glr_bwd(&s, call.stream)) return none();
     return give({&dx, &dr, &di, &dlam, &dh0});
 }
 
@@ -260,7 +266,7 @@ BINDING(layer_norm_fwd, 7) {
     at::Tensor y, mean, rstd;
     const auto lead = x->sizes().slice(0, x->dim() - 1);
     s.y = call.out(a[4], y, x->scalar_type(), x->sizes(), 1);
-    if (a[5] == Py_True) {
+    if (call.flag(a[5])) {
         s.mean = call.out<float>(Py_None, mean, at::kFloat, lead, 4);
         s.rstd = call.out<float>(Py_None, rstd, at::kFloat, lead, 4);
     }
@@ -282,8 +288,8 @@ BINDING(layer_norm_bwd, 9) {
     s.f.w = call.dense<float>(a[4], at::kFloat, {s.f.D}, 4, true);
     at::Tensor dx, dw, db, scratch;
     s.dx = call.out(a[5], dx, x->scalar_type(), x->sizes(), 1);
-    if (a[6] == Py_True) s.dw = call.out<float>(Py_None, dw, at::kFloat, {s.f.D}, 4);
-    if (a[7] == Py_True) s.db = call.out<float>(Py_None, db, at::kFloat, {s.f.D}, 4);
+    if (call.flag(a[6])) s.dw = call.out<float>(Py_None, dw, at::kFloat, {s.f.D}, 4);
+    if (call.flag(a[7])) s.db = call.out<float>(Py_None, db, at::kFloat, {s.f.D}, 4);
     if (!call.good) return none();
     if (s.dw || s.db) {
         s.workspace_bytes = lib.layernorm_workspace_bytes(s.f.rows, s.f.D);
