@@ -1003,7 +1003,7 @@ def glr_fwd(x, rgate, igate, lam, h0=None, *, c=8.0, return_last_state=False, sa
     holds the status word for poll_status; without one the call uses scratch of its own and reports no status.
     Returns (y, h_last or None, ckpt or None)."""
     if stream is None and ckpt is None and (_short or _short_way()):
-        r = _short.glr_fwd(x, rgate, igate, lam, c, h0, y, h_last, None, return_last_state, save_ckpt, *_space(workspace))
+        r = _short.glr_fwd(x, rgate, igate, lam, c, h0, y, h_last, None, return_last_state, save_ckpt, _buf(workspace))
         if r is not None:
             return r
     dev, io, code = _io_of(x, "x", 3, "the gated linear recurrence")
@@ -1025,7 +1025,7 @@ def glr_bwd(x, rgate, igate, lam, dy, ckpt, *, c=8.0, dh_last=None, return_dh0=F
     well). Returns a dict with dx, drgate, digate [B, L, D] in x's dtype, dlam [D] fp32 and, if asked, dh0 [B, D] fp32.
     ``inplace`` writes dx into dy."""
     if stream is None and not inplace and not out and (_short or _short_way()):
-        r = _short.glr_bwd(x, rgate, igate, lam, c, dy, ckpt, dh_last, return_dh0, *_space(workspace))
+        r = _short.glr_bwd(x, rgate, igate, lam, c, dy, ckpt, dh_last, return_dh0, _buf(workspace))
         if r is not None:
             o = {"dx": r[0], "drgate": r[1], "digate": r[2], "dlam": r[3]}
             if return_dh0:
@@ -1056,7 +1056,7 @@ def glr_step(state, x_t, rgate_t, igate_t, lam, *, c=8.0, y_t=None, workspace=No
     """One token of the gated linear recurrence for every channel: x_t, rgate_t, igate_t [B, D] (dense or column slices);
     ``state`` [B, D] fp32 is updated in place. Returns y_t [B, D] in x_t's dtype."""
     if stream is None and (_short or _short_way()):
-        r = _short.glr_step(state, x_t, rgate_t, igate_t, lam, c, y_t, _status(workspace))
+        r = _short.glr_step(state, x_t, rgate_t, igate_t, lam, c, y_t, _buf(workspace))
         if r is not None:
             return r
     dev, io, code = _io_of(x_t, "x_t", 2, "the gated linear recurrence")
@@ -1068,7 +1068,7 @@ def glr_step(state, x_t, rgate_t, igate_t, lam, *, c=8.0, y_t=None, workspace=No
     y_t, yp = _out(y_t, "y_t", stream, shape, io, dev)
     _glr_step(_raw_stream(dev, stream), B, D, xs, rs, is_, code, c, xp, rp, ip,
               _at(_must(lam, "lam"), "lam", (D,), f32, dev), _at(_must(state, "state"), "state", shape, f32, dev),
-              yp, 0 if workspace is None else workspace.buf.data_ptr())
+              yp, _status(workspace, dev))
     return y_t
 
 
@@ -1097,13 +1097,17 @@ def _dense(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous (the library reads raw row-major memory)")
 
 
-def _space(workspace):
-    """Address and size of a caller's workspace; zeros for none."""
-    return (0, 0) if workspace is None else (workspace.buf.data_ptr(), workspace.nbytes)
+def _buf(workspace):
+    return None if workspace is None else workspace.buf
 
 
-def _status(workspace):
-    return 0 if workspace is None else workspace.buf.data_ptr()
+def _status(workspace, device):
+    """Address of the workspace a call leaves its status word in (0 for none)."""
+    if workspace is None:
+        return 0
+    if workspace.buf.device != device:
+        raise ValueError(f"workspace is on {workspace.buf.device}, expected {device}")
+    return workspace.buf.data_ptr()
 
 
 def _norm_x(x):
@@ -1122,7 +1126,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, save_stats=Tr
     or None. Returns (y, mean, rstd): y dense in x's dtype, mean and rstd [...] fp32 for layer_norm_bwd (None unless
     ``save_stats``). ``workspace`` takes the status word for poll_status."""
     if stream is None and (_short or _short_way()):
-        r = _short.layer_norm_fwd(x, weight, bias, eps, y, save_stats, _status(workspace))
+        r = _short.layer_norm_fwd(x, weight, bias, eps, y, save_stats, _buf(workspace))
         if r is not None:
             return r
     dev, io, code, shape, D, lead, rows, stride = _norm_x(x)
@@ -1134,7 +1138,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, save_stats=Tr
         mean, mp = _out(None, "mean", stream, lead, f32, dev)
         rstd, rp = _out(None, "rstd", stream, lead, f32, dev)
     _layernorm_fwd(_raw_stream(dev, stream), rows, D, stride, code, eps, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
-                   _at(bias, "bias", (D,), f32, dev, 0), yp, mp, rp, _status(workspace))
+                   _at(bias, "bias", (D,), f32, dev, 0), yp, mp, rp, _status(workspace, dev))
     return y, mean, rstd
 
 
@@ -1144,7 +1148,7 @@ def layer_norm_bwd(x, dy, mean, rstd, weight=None, *, dx=None, want_dweight=True
     [..., D] in x's dtype and, unless switched off, dweight and dbias [D] fp32 (summed over the rows in a fixed order).
     dx may be dy or a dense x."""
     if stream is None and (_short or _short_way()):
-        r = _short.layer_norm_bwd(x, dy, mean, rstd, weight, dx, want_dweight, want_dbias, _status(workspace))
+        r = _short.layer_norm_bwd(x, dy, mean, rstd, weight, dx, want_dweight, want_dbias, _buf(workspace))
         if r is not None:
             return {"dx": r[0], "dweight": r[1], "dbias": r[2]}
     dev, io, code, shape, D, lead, rows, stride = _norm_x(x)
@@ -1156,7 +1160,7 @@ def layer_norm_bwd(x, dy, mean, rstd, weight=None, *, dx=None, want_dweight=True
     _part, partp = _out(None, "partial sums", stream, (n,), torch.uint8, dev) if n else (None, 0)
     _layernorm_bwd(_raw_stream(dev, stream), rows, D, stride, code, 0.0, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
                    0, 0, _at(_must(mean, "mean"), "mean", lead, f32, dev, 0), _at(_must(rstd, "rstd"), "rstd", lead, f32, dev, 0),
-                   _status(workspace), _at(_must(dy, "dy"), "dy", shape, io, dev, 0), dxp, dwp, dbp, partp, n)
+                   _status(workspace, dev), _at(_must(dy, "dy"), "dy", shape, io, dev, 0), dxp, dwp, dbp, partp, n)
     return {"dx": dx, "dweight": dw, "dbias": db}
 
 
@@ -1182,7 +1186,7 @@ def embed_fwd(ids, weight, scale=1.0, *, out=None, workspace=None, stream=None):
     int32; weight [V, D] fp32 or bf16; returns out [..., D] in weight's dtype. An id outside [0, V) gives a row of zeros
     and, with a ``workspace``, the status -9 from poll_status."""
     if stream is None and (_short or _short_way()):
-        r = _short.embed_fwd(ids, weight, scale, out, _status(workspace))
+        r = _short.embed_fwd(ids, weight, scale, out, _buf(workspace))
         if r is not None:
             return r
     dev, ids64 = _ids(ids)
@@ -1191,7 +1195,7 @@ def embed_fwd(ids, weight, scale=1.0, *, out=None, workspace=None, stream=None):
     shape = ids.shape + (D,)
     out, outp = _out(out, "out", stream, shape, io, dev, 0)
     _embed_fwd(_raw_stream(dev, stream), ids.numel(), V, D, code, ids64, scale, 0, ids.data_ptr(),
-               _at(weight, "weight", (V, D), io, dev, 0), outp, _status(workspace))
+               _at(weight, "weight", (V, D), io, dev, 0), outp, _status(workspace, dev))
     return out
 
 
@@ -1200,7 +1204,7 @@ def embed_bwd(ids, dy, V, scale=1.0, *, padding_idx=None, dweight=None, workspac
     row written (zeros where no token names it, and for ``padding_idx``); the tokens sorted by id and summed in their
     order, the same bits every time. dy [..., D] fp32 or bf16. ``workspace`` takes the status word."""
     if stream is None and (_short or _short_way()):
-        r = _short.embed_bwd(ids, dy, V, scale, -1 if padding_idx is None else padding_idx, dweight, _status(workspace))
+        r = _short.embed_bwd(ids, dy, V, scale, -1 if padding_idx is None else padding_idx, dweight, _buf(workspace))
         if r is not None and (padding_idx is None or padding_idx >= 0):
             return r
     dev, ids64 = _ids(ids)
@@ -1217,7 +1221,7 @@ def embed_bwd(ids, dy, V, scale=1.0, *, padding_idx=None, dweight=None, workspac
     n = embed_workspace_bytes(tokens, V, D)
     _ws, wsp = _out(None, "scratch", stream, (n,), torch.uint8, dev) if n else (None, 0)
     _embed_bwd(_raw_stream(dev, stream), tokens, V, D, pad, code, ids64, scale, 0, ids.data_ptr(),
-               _at(dy, "dy", ids.shape + (D,), io, dev, 0), dwp, wsp, n, _status(workspace))
+               _at(dy, "dy", ids.shape + (D,), io, dev, 0), dwp, wsp, n, _status(workspace, dev))
     return dweight
 
 
@@ -1253,7 +1257,7 @@ def w4_matvec(x, qweight, scales, bias=None, *, out_dtype=torch.bfloat16, out=No
     [N, K/group] bf16 as w4_quantize makes them (the group is read off their shapes); bias [N] fp32. Returns y [..., N]
     bf16 or fp32 (``out_dtype``). ``workspace`` (of w4_workspace_bytes) takes the status word."""
     if stream is None and out_dtype in _IO and (out is None or out.dtype == out_dtype) and (_short or _short_way()):
-        r = _short.w4_matvec(x, qweight, scales, bias, out, out_dtype is torch.float32, *_space(workspace))
+        r = _short.w4_matvec(x, qweight, scales, bias, out, out_dtype is torch.float32, _buf(workspace))
         if r is not None:
             return r
     dev, bf = _io_of(x, "x", None, "the product")[0], torch.bfloat16

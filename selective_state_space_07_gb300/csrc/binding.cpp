@@ -118,13 +118,23 @@ struct Call {
 
 double number(PyObject* o) { return PyFloat_AsDouble(o); }  // (-1 with an error set if it is none: the caller looks)
 
-// The caller's workspace, as (address, bytes) from Python: 0 for none.
+// The buffer of the caller's workspace, on the call's device; None: none.
 struct Space {
     void* at;
     size_t bytes;
 };
-Space space(PyObject* at, PyObject* bytes) {
-    return {reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(at)), (size_t)PyLong_AsUnsignedLongLong(bytes)};
+Space space(Call& call, PyObject* o) {
+    if (!call.good || o == Py_None) return {nullptr, 0};
+    if (!THPVariable_CheckExact(o)) return call.fail(), Space{nullptr, 0};
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.scalar_type() != at::kByte || t.device() != call.device || t.dim() != 1 || !t.is_contiguous()) return call.fail(), Space{nullptr, 0};
+    return {t.data_ptr(), (size_t)t.numel()};
+}
+// ... of which the status word is wanted only.
+void* status(Call& call, PyObject* o) {
+    const Space w = space(call, o);
+    if (w.at && w.bytes < 256) call.fail();
+    return w.at;
 }
 
 PyObject* none() {
@@ -153,7 +163,7 @@ PyObject* give(std::initializer_list<const at::Tensor*> tensors) {
     }                                                                            \
     PyObject* name##_body(PyObject* const* a)
 
-// state, x, rgate, igate, lam, c, y or None, status address
+// state, x, rgate, igate, lam, c, y or None, workspace or None
 BINDING(glr_step, 8) {
     Call call;
     const at::Tensor* x = call.lead(a[1], 2);
@@ -172,7 +182,7 @@ BINDING(glr_step, 8) {
     s.state = call.dense<float>(a[0], at::kFloat, shape, 16);
     at::Tensor y;
     s.y_t = call.out(a[6], y, type, shape, 16);
-    s.workspace = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(a[7]));
+    s.workspace = status(call, a[7]);
     if (!call.good || PyErr_Occurred() || lib.glr_step(&s, call.stream)) return none();
     return THPVariable_Wrap(y);
 }
@@ -192,8 +202,9 @@ bool glr_inputs(Call& call, PyObject* const* a, ssm_glr_args& s, const at::Tenso
     return call.good;
 }
 // The caller's workspace, or scratch for this call.
-bool glr_space(Call& call, PyObject* at, PyObject* bytes, ssm_glr_args& s, at::Tensor& scratch) {
-    const Space w = space(at, bytes);
+bool glr_space(Call& call, PyObject* o, ssm_glr_args& s, at::Tensor& scratch) {
+    const Space w = space(call, o);
+    if (!call.good) return false;
     const size_t need = lib.glr_workspace_bytes(s.B, s.L, s.D);
     s.workspace = w.at, s.workspace_bytes = w.bytes;
     if (!w.at) {
@@ -203,8 +214,8 @@ bool glr_space(Call& call, PyObject* at, PyObject* bytes, ssm_glr_args& s, at::T
     return !PyErr_Occurred() && s.workspace_bytes >= need;
 }
 
-// x, rgate, igate, lam, c, h0, y, h_last, ckpt (each or None), want h_last, want ckpt, workspace address, bytes
-BINDING(glr_fwd, 13) {
+// x, rgate, igate, lam, c, h0, y, h_last, ckpt (each or None), want h_last, want ckpt, workspace or None
+BINDING(glr_fwd, 12) {
     Call call;
     ssm_glr_args s{};
     const at::Tensor* x;
@@ -215,12 +226,12 @@ BINDING(glr_fwd, 13) {
     if (a[7] != Py_None || call.flag(a[9])) s.h_last = call.out<float>(a[7], last, at::kFloat, {s.B, s.D}, 16);
     if (a[8] != Py_None) return none();  // (a buffer of the caller's may have any shape)
     if (call.flag(a[10])) s.ckpt = call.out<float>(Py_None, ckpt, at::kFloat, {s.B, (s.L + kSavedEvery - 1) / kSavedEvery, s.D}, 16);
-    if (!call.good || !glr_space(call, a[11], a[12], s, scratch) || lib.glr_fwd(&s, call.stream)) return none();
+    if (!call.good || !glr_space(call, a[11], s, scratch) || lib.glr_fwd(&s, call.stream)) return none();
     return give({&y, &last, &ckpt});
 }
 
-// x, rgate, igate, lam, c, dy, ckpt, dh_last or None, want dh0, workspace address, bytes
-BINDING(glr_bwd, 11) {
+// x, rgate, igate, lam, c, dy, ckpt, dh_last or None, want dh0, workspace or None
+BINDING(glr_bwd, 10) {
     Call call;
     ssm_glr_bwd_args s{};
     const at::Tensor* x;
@@ -238,7 +249,7 @@ BINDING(glr_bwd, 11) {
     s.digate = call.out(Py_None, di, type, shape, 16);
     s.dlam = call.out<float>(Py_None, dlam, at::kFloat, {f.D}, 16);
     if (call.flag(a[8])) s.dh0 = call.out<float>(Py_None, dh0, at::kFloat, {f.B, f.D}, 16);
-    if (!call.good || !glr_space(call, a[9], a[10], s.f, scratch) || lib.glr_bwd(&s, call.stream)) return none();
+    if (!call.good || !glr_space(call, a[9], s.f, scratch) || lib.glr_bwd(&s, call.stream)) return none();
     return give({&dx, &dr, &di, &dlam, &dh0});
 }
 
@@ -254,7 +265,7 @@ bool norm_inputs(Call& call, PyObject* const* a, ssm_layernorm_args& s, const at
     return true;
 }
 
-// x, weight, bias, eps, y or None, want statistics, status address
+// x, weight, bias, eps, y or None, want statistics, workspace or None
 BINDING(layer_norm_fwd, 7) {
     Call call;
     ssm_layernorm_args s{};
@@ -270,12 +281,12 @@ BINDING(layer_norm_fwd, 7) {
         s.mean = call.out<float>(Py_None, mean, at::kFloat, lead, 4);
         s.rstd = call.out<float>(Py_None, rstd, at::kFloat, lead, 4);
     }
-    s.status = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(a[6]));
+    s.status = status(call, a[6]);
     if (!call.good || PyErr_Occurred() || lib.layernorm_fwd(&s, call.stream)) return none();
     return give({&y, &mean, &rstd});
 }
 
-// x, dy, mean, rstd, weight or None, dx or None, want dweight, want dbias, status address
+// x, dy, mean, rstd, weight or None, dx or None, want dweight, want dbias, workspace or None
 BINDING(layer_norm_bwd, 9) {
     Call call;
     ssm_layernorm_bwd_args s{};
@@ -290,6 +301,7 @@ BINDING(layer_norm_bwd, 9) {
     s.dx = call.out(a[5], dx, x->scalar_type(), x->sizes(), 1);
     if (call.flag(a[6])) s.dw = call.out<float>(Py_None, dw, at::kFloat, {s.f.D}, 4);
     if (call.flag(a[7])) s.db = call.out<float>(Py_None, db, at::kFloat, {s.f.D}, 4);
+    s.f.status = status(call, a[8]);
     if (!call.good) return none();
     if (s.dw || s.db) {
         s.workspace_bytes = lib.layernorm_workspace_bytes(s.f.rows, s.f.D);
@@ -298,7 +310,6 @@ BINDING(layer_norm_bwd, 9) {
             s.workspace = scratch.data_ptr();
         }
     }
-    s.f.status = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(a[8]));
     if (PyErr_Occurred() || lib.layernorm_bwd(&s, call.stream)) return none();
     return give({&dx, &dw, &db});
 }
@@ -310,7 +321,7 @@ const at::Tensor* ids_of(Call& call, PyObject* o, int32_t& ids64) {
     return ids64 || t->scalar_type() == at::kInt ? t : nullptr;
 }
 
-// ids, weight, scale, out or None, status address
+// ids, weight, scale, out or None, workspace or None
 BINDING(embed_fwd, 5) {
     Call call;
     ssm_embed_args s{};
@@ -325,12 +336,12 @@ BINDING(embed_fwd, 5) {
     shape.push_back(s.D);
     at::Tensor out;
     s.out = call.out(a[3], out, W.scalar_type(), shape, 1);
-    s.status = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(a[4]));
+    s.status = status(call, a[4]);
     if (!call.good || PyErr_Occurred() || lib.embed_fwd(&s, call.stream)) return none();
     return THPVariable_Wrap(out);
 }
 
-// ids, dy, V, scale, padding id (-1: none), dweight or None, status address
+// ids, dy, V, scale, padding id (-1: none), dweight or None, workspace or None
 BINDING(embed_bwd, 7) {
     Call call;
     ssm_embed_bwd_args s{};
@@ -348,19 +359,19 @@ BINDING(embed_bwd, 7) {
     s.dy = call.dense(a[1], dy.scalar_type(), shape, 1);
     at::Tensor dw, scratch;
     s.dW = call.out<float>(a[5], dw, at::kFloat, {s.V, s.D}, 4);
+    s.status = status(call, a[6]);
     if (!call.good) return none();
     s.workspace_bytes = lib.embed_workspace_bytes(s.tokens, s.V, s.D);
     if (s.workspace_bytes) {
         scratch = call.make({(int64_t)s.workspace_bytes}, at::kByte);
         s.workspace = scratch.data_ptr();
     }
-    s.status = reinterpret_cast<void*>(PyLong_AsUnsignedLongLong(a[6]));
     if (PyErr_Occurred() || lib.embed_bwd(&s, call.stream)) return none();
     return THPVariable_Wrap(dw);
 }
 
-// x, qweight, scales, bias or None, out or None, out is fp32, workspace address, bytes
-BINDING(w4_matvec, 8) {
+// x, qweight, scales, bias or None, out or None, out is fp32, workspace or None
+BINDING(w4_matvec, 7) {
     Call call;
     ssm_w4_args s{};
     const at::Tensor* x = call.lead(a[0], -1);
@@ -381,7 +392,7 @@ BINDING(w4_matvec, 8) {
     shape.push_back(s.N);
     at::Tensor y, scratch;
     s.y = call.out(a[4], y, type, shape, type == at::kFloat ? 4 : 2);
-    const Space w = space(a[6], a[7]);
+    const Space w = space(call, a[6]);
     if (!call.good || PyErr_Occurred()) return none();
     const size_t need = lib.w4_workspace_bytes(s.M, s.N, s.K);
     s.workspace = w.at, s.workspace_bytes = w.bytes;

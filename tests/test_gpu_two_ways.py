@@ -45,3 +45,44 @@ def test_switches_without_a_truth_value(ssm, way):
     x = torch.randn(3, 8, device="cuda")
     with pytest.raises(ValueError):
         ssm.layer_norm_fwd(x, save_stats=np.ones(2))
+
+
+def calls(ssm, ws):
+    """Every operator once with this workspace, as (call, its outputs)."""
+    x, lam = torch.randn(4, 64, device="cuda"), torch.zeros(64, device="cuda")
+    s = x[None].contiguous()
+    new = lambda *shape: torch.full(shape, 7.0, device="cuda")  # noqa: E731
+    ck = ssm.glr_fwd(s, s, s, lam)[2]
+    _, mean, rstd = ssm.layer_norm_fwd(x)
+    ids = torch.tensor([1, 2, 3, 0], device="cuda")
+    q, sc = ssm.w4_quantize(x, 32)
+    y, st, h, d, e, g, p, o = new(1, 4, 64), new(4, 64), new(1, 64), new(4, 64), new(4, 64), new(9, 64), new(4, 64), new(4, 4)
+    return [
+        (lambda: ssm.glr_fwd(s, s, s, lam, y=y, h_last=h, workspace=ws), (y, h)),
+        (lambda: ssm.glr_bwd(s, s, s, lam, s, ck, workspace=ws), ()),
+        (lambda: ssm.glr_bwd(s, s, s, lam, s, ck, out={"dx": y}, workspace=ws), (y,)),
+        (lambda: ssm.glr_step(st, x, x, x, lam, y_t=p, workspace=ws), (st, p)),
+        (lambda: ssm.layer_norm_fwd(x, y=d, workspace=ws), (d,)),
+        (lambda: ssm.layer_norm_bwd(x, x, mean, rstd, dx=e, workspace=ws), (e,)),
+        (lambda: ssm.embed_fwd(ids, x, out=p, workspace=ws), (p,)),
+        (lambda: ssm.embed_bwd(ids, x, 9, dweight=g, workspace=ws), (g,)),
+        (lambda: ssm.w4_matvec(x.bfloat16(), q, sc, out=o, out_dtype=torch.float32, workspace=ws), (o,)),
+    ]
+
+
+def test_a_workspace_on_another_device_is_refused(ssm, way):
+    # before anything is launched: given outputs keep what they hold
+    for call, outs in calls(ssm, ssm.Workspace.of_bytes(1 << 16, "cpu")):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
+        assert all(bool((t == 7.0).all()) for t in outs)
+
+
+def test_a_workspace_on_the_same_device_is_used(ssm, way):
+    ws = ssm.Workspace.of_bytes(1 << 16, "cuda")
+    for call, _ in calls(ssm, ws):
+        call()
+        assert ssm.poll_status(ws) == 0
+    bad = torch.tensor([1, -1, 3, 0], device="cuda")
+    ssm.embed_fwd(bad, torch.randn(4, 64, device="cuda"), workspace=ws)
+    assert ssm.poll_status(ws) == -9
