@@ -347,9 +347,19 @@ class Workspace:
         return self.nbytes >= workspace_bytes(B, L, D, N)
 
 
+def _status(workspace, device):
+    """Address of the workspace a call leaves its status word in (0 for none)."""
+    if workspace is None:
+        return 0
+    if workspace.buf.device != device:
+        raise ValueError(f"workspace is on {workspace.buf.device}, expected {device}")
+    return workspace.buf.data_ptr()
+
+
 def _ws(ws, B, L, D, device):
     if ws is None or not ws.fits(B, L, D):
-        ws = Workspace(B, L, D, device)
+        return Workspace(B, L, D, device)
+    _status(ws, device)
     return ws
 
 
@@ -526,7 +536,7 @@ def step(state, x_t, dt_t, A, Bm_t, Cm_t, z_t=None, Dskip=None, dt_bias=None, de
     args = StepArgs(B=B, D=D, N=N, io_dtype=_IO[io], delta_softplus=int(bool(delta_softplus)), x_t=_p(x_t),
                     z_t=_p(z_t), Bm_t=_p(Bm_t), Cm_t=_p(Cm_t), dt_t=_p(dt_t), dt_bias=_p(dt_bias), A=_p(A),
                     Dskip=_p(Dskip), state=_p(state), y_t=_p(y_t),
-                    workspace=None if workspace is None else workspace.buf.data_ptr(), nsplit=nsplit,
+                    workspace=_status(workspace, dev), nsplit=nsplit,
                     bc_stride=_bc_stride_pair(Bm_t, Cm_t, B, N))
     _check(lib().ssm_step(ctypes.byref(args), _stream(dev, stream)), "ssm_step")
     return y_t
@@ -563,7 +573,7 @@ def _conv_struct(xin, w, bias, state_in, x, state_out, workspace):
     _opt(state_out, "state_out", (B, D, K - 1), torch.float32, dev)
     return ConvArgs(B=B, L=L, D=D, K=K, io_dtype=_IO[io], xin=_p(xin), w=_p(w), bias=_p(bias),
                     state_in=_p(state_in), x=_p(x), state_out=_p(state_out),
-                    workspace=None if workspace is None else workspace.buf.data_ptr())
+                    workspace=_status(workspace, dev))
 
 
 def conv1d_fwd(xin, w, bias=None, state_in=None, *, x=None, state_out=None, want_state=False, workspace=None,
@@ -633,7 +643,7 @@ def _dtproj_struct(a, w, bias, softplus, delta, workspace):
     _opt(delta, "delta", lead + (D,), torch.float32, dev)
     args = DtProjArgs(M=M, D=D, R=R, a_stride=0 if stride == R else stride, softplus=int(bool(softplus)),
                       a=_p(a), w=_p(w), bias=_p(bias), delta=_p(delta),
-                      workspace=None if workspace is None else workspace.buf.data_ptr())
+                      workspace=_status(workspace, dev))
     return args, lead, D
 
 
@@ -692,7 +702,7 @@ def gdn2_fwd(q, k, v, g, b, w, state=None, scale=None, *, out=None, state_out=No
     args = Gdn2Args(B=Bn, H=H, T=T, K=K, V=V, chunk=GDN2_CHUNK,
                     scale=float(K ** -0.5 if scale is None else scale),
                     q=_p(q), k=_p(k), v=_p(v), g=_p(g), b=_p(b), w=_p(w), state_in=_p(state), out=_p(out),
-                    state_out=_p(state_out), workspace=None if workspace is None else workspace.buf.data_ptr())
+                    state_out=_p(state_out), workspace=_status(workspace, dev))
     _check(lib().gdn2_chunk_fwd(ctypes.byref(args), _stream(dev, stream)), "gdn2_chunk_fwd")
     return out, state_out
 
@@ -719,7 +729,7 @@ def gdn2_step(q, k, v, g, b, w, state, scale=None, *, out=None, workspace=None, 
     _need(out, "out", (Bn, H, V), bf, dev)
     args = Gdn2StepArgs(B=Bn, H=H, K=K, V=V, scale=float(K ** -0.5 if scale is None else scale), q=_p(q), k=_p(k),
                         v=_p(v), g=_p(g), b=_p(b), w=_p(w), state=_p(state), out=_p(out),
-                        workspace=None if workspace is None else workspace.buf.data_ptr())
+                        workspace=_status(workspace, dev))
     _check(lib().gdn2_step(ctypes.byref(args), _stream(dev, stream)), "gdn2_step")
     return out
 
@@ -773,7 +783,7 @@ def mlstm_fwd(q, k, v, igate, fgate, state=None, scale=None, *, norm_weight=None
                      q=_p(q), k=_p(k), v=_p(v), igate=_p(igate), fgate=_p(fgate),
                      C_in=_p(si[0]), n_in=_p(si[1]), m_in=_p(si[2]), norm_weight=_p(norm_weight), h=_p(h),
                      C_out=_p(so[0]), n_out=_p(so[1]), m_out=_p(so[2]),
-                     workspace=None if workspace is None else workspace.buf.data_ptr())
+                     workspace=_status(workspace, dev))
     _check(lib().mlstm_chunk_fwd(ctypes.byref(args), _stream(dev, stream)), "mlstm_chunk_fwd")
     return h, state_out
 
@@ -808,7 +818,7 @@ def mlstm_step(q, k, v, igate, fgate, state, scale=None, *, norm_weight=None, no
     args = MlstmStepArgs(B=Bn, H=H, K=K, V=V, scale=float(K ** -0.5 if scale is None else scale),
                          norm_eps=float(norm_eps), q=_p(q), k=_p(k), v=_p(v), igate=_p(igate), fgate=_p(fgate),
                          C=_p(state[0]), n=_p(state[1]), m=_p(state[2]), norm_weight=_p(norm_weight), h=_p(h),
-                         workspace=None if workspace is None else workspace.buf.data_ptr())
+                         workspace=_status(workspace, dev))
     _check(lib().mlstm_step(ctypes.byref(args), _stream(dev, stream)), "mlstm_step")
     return h
 
@@ -1099,15 +1109,6 @@ def _dense(t, name, shape, dtype, device):
 
 def _buf(workspace):
     return None if workspace is None else workspace.buf
-
-
-def _status(workspace, device):
-    """Address of the workspace a call leaves its status word in (0 for none)."""
-    if workspace is None:
-        return 0
-    if workspace.buf.device != device:
-        raise ValueError(f"workspace is on {workspace.buf.device}, expected {device}")
-    return workspace.buf.data_ptr()
 
 
 def _norm_x(x):

@@ -18,3 +18,10 @@ def test_a_status_word_lies_on_the_calls_device(ssm):
     assert ssm._status(ws, torch.device("cpu")) == ws.buf.data_ptr()
     with pytest.raises(ValueError, match="workspace is on cpu"):
         ssm._status(ws, torch.device("cuda", 0))
+
+
+def test_a_scans_workspace_lies_on_the_calls_device(ssm):
+    ws = ssm.Workspace(1, 8, 8, "cpu")
+    assert ssm._ws(ws, 1, 8, 8, torch.device("cpu")) is ws
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        ssm._ws(ws, 1, 8, 8, torch.device("cuda", 0))
