@@ -296,9 +296,35 @@ def _opt(t, name, shape, dtype, device):
     return t
 
 
-def _stream(device, stream):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(device, stream):
+    """The address of the stream a call on `device` runs on."""
+    if device.type != "cuda":
+        raise ValueError(f"expected a CUDA device, got {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on_device(f, device, stream, *args):
+    """f(*args, address of the stream) with `device` the current one: kernels launch on the current device, and the
+    address of a default stream (0) means that device's."""
+    s = _raw_stream(device, stream)
+    if device.index == torch.cuda.current_device():
+        return f(*args, s)
+    with torch.cuda.device(device):
+        return f(*args, s)
+
+
+def _launch(name, device, stream, *args):
+    """The C entry point `name`, whose last argument is the stream."""
+    _check(_on_device(getattr(lib(), name), device, stream, *args), name)
 
 
 def workspace_bytes(B: int, L: int, D: int, N: int = 16) -> int:
@@ -461,7 +487,7 @@ def scan_fwd(x, dt, A, Bm, Cm, z=None, Dskip=None, dt_bias=None, h0=None, delta_
     ws = _ws(workspace, B, L, D, dev)
     args = _fwd_struct(x, dt, A, Bm, Cm, z, Dskip, dt_bias, h0, delta_softplus, y, h_last, ckpt, ws, nsplit,
                        groups)
-    _check(lib().ssm_scan_fwd(ctypes.byref(args), _stream(dev, stream)), "ssm_scan_fwd")
+    _launch("ssm_scan_fwd", dev, stream, ctypes.byref(args))
     return y, h_last, ckpt, ws
 
 
@@ -505,7 +531,7 @@ def scan_bwd(x, dt, A, Bm, Cm, dy, ckpt, z=None, Dskip=None, dt_bias=None, h0=No
     args = BwdArgs(f=fa, dy=_p(dy), dh_last=_p(dh_last), dx=_p(o["dx"]), dz=_p(o.get("dz")),
                    d_dt=_p(o["d_dt"]), dA=_p(o["dA"]), dD=_p(o["dD"]), d_dt_bias=_p(o["d_dt_bias"]),
                    dB=_p(o["dB"]), dC=_p(o["dC"]), dh0=_p(o.get("dh0")))
-    _check(lib().ssm_scan_bwd(ctypes.byref(args), _stream(dev, stream)), "ssm_scan_bwd")
+    _launch("ssm_scan_bwd", dev, stream, ctypes.byref(args))
     o["workspace"] = ws
     return o
 
@@ -538,7 +564,7 @@ def step(state, x_t, dt_t, A, Bm_t, Cm_t, z_t=None, Dskip=None, dt_bias=None, de
                     Dskip=_p(Dskip), state=_p(state), y_t=_p(y_t),
                     workspace=_status(workspace, dev), nsplit=nsplit,
                     bc_stride=_bc_stride_pair(Bm_t, Cm_t, B, N))
-    _check(lib().ssm_step(ctypes.byref(args), _stream(dev, stream)), "ssm_step")
+    _launch("ssm_step", dev, stream, ctypes.byref(args))
     return y_t
 
 
@@ -548,8 +574,7 @@ def dA_log_grad(dA, A, out=None, stream=None):
     _need(dA, "dA", tuple(A.shape), torch.float32, A.device)
     out = torch.empty_like(A) if out is None else out
     _need(out, "out", tuple(A.shape), torch.float32, A.device)
-    _check(lib().ssm_dA_log_grad(_p(dA), _p(A), _p(out), A.numel(), _stream(A.device, stream)),
-           "ssm_dA_log_grad")
+    _launch("ssm_dA_log_grad", A.device, stream, _p(dA), _p(A), _p(out), A.numel())
     return out
 
 
@@ -589,7 +614,7 @@ def conv1d_fwd(xin, w, bias=None, state_in=None, *, x=None, state_out=None, want
     if state_out is None and want_state:
         state_out = torch.empty(B, D, max(K - 1, 0), dtype=torch.float32, device=xin.device)
     args = _conv_struct(xin, w, bias, state_in, x, state_out, workspace)
-    _check(lib().ssm_conv1d_fwd(ctypes.byref(args), _stream(xin.device, stream)), "ssm_conv1d_fwd")
+    _launch("ssm_conv1d_fwd", xin.device, stream, ctypes.byref(args))
     return x, state_out
 
 
@@ -608,7 +633,7 @@ def conv1d_bwd(xin, w, dx, bias=None, state_in=None, *, dxin=None, want_dstate=F
     dbias = torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None
     dstate = torch.empty(B, D, max(K - 1, 0), dtype=torch.float32, device=dev) if want_dstate else None
     args = ConvBwdArgs(f=f, dx=_p(dx), dxin=_p(dxin), dw=_p(dw), dbias=_p(dbias), dstate_in=_p(dstate))
-    _check(lib().ssm_conv1d_bwd(ctypes.byref(args), _stream(dev, stream)), "ssm_conv1d_bwd")
+    _launch("ssm_conv1d_bwd", dev, stream, ctypes.byref(args))
     return {"dxin": dxin, "dw": dw, "dbias": dbias, "dstate_in": dstate}
 
 
@@ -655,7 +680,7 @@ def dtproj_fwd(a, w, bias=None, softplus=True, *, delta=None, workspace=None, st
     lead, D = tuple(a.shape[:-1]), w.shape[0]
     delta = torch.empty(lead + (D,), dtype=torch.float32, device=a.device) if delta is None else delta
     args, _, _ = _dtproj_struct(a, w, bias, softplus, delta, workspace)
-    _check(lib().ssm_dtproj_fwd(ctypes.byref(args), _stream(a.device, stream)), "ssm_dtproj_fwd")
+    _launch("ssm_dtproj_fwd", a.device, stream, ctypes.byref(args))
     return delta
 
 
@@ -669,7 +694,7 @@ def dtproj_bwd(a, w, ddelta, bias=None, softplus=True, *, dpre=None, inplace=Fal
     _need(dpre, "dpre", lead + (D,), torch.float32, a.device)
     dbias = torch.empty(D, dtype=torch.float32, device=a.device) if bias is not None else None
     bargs = DtProjBwdArgs(f=args, ddelta=_p(ddelta), dpre=_p(dpre), dbias=_p(dbias))
-    _check(lib().ssm_dtproj_bwd(ctypes.byref(bargs), _stream(a.device, stream)), "ssm_dtproj_bwd")
+    _launch("ssm_dtproj_bwd", a.device, stream, ctypes.byref(bargs))
     return {"dpre": dpre, "dbias": dbias}
 
 
@@ -703,7 +728,7 @@ def gdn2_fwd(q, k, v, g, b, w, state=None, scale=None, *, out=None, state_out=No
                     scale=float(K ** -0.5 if scale is None else scale),
                     q=_p(q), k=_p(k), v=_p(v), g=_p(g), b=_p(b), w=_p(w), state_in=_p(state), out=_p(out),
                     state_out=_p(state_out), workspace=_status(workspace, dev))
-    _check(lib().gdn2_chunk_fwd(ctypes.byref(args), _stream(dev, stream)), "gdn2_chunk_fwd")
+    _launch("gdn2_chunk_fwd", dev, stream, ctypes.byref(args))
     return out, state_out
 
 
@@ -730,7 +755,7 @@ def gdn2_step(q, k, v, g, b, w, state, scale=None, *, out=None, workspace=None, 
     args = Gdn2StepArgs(B=Bn, H=H, K=K, V=V, scale=float(K ** -0.5 if scale is None else scale), q=_p(q), k=_p(k),
                         v=_p(v), g=_p(g), b=_p(b), w=_p(w), state=_p(state), out=_p(out),
                         workspace=_status(workspace, dev))
-    _check(lib().gdn2_step(ctypes.byref(args), _stream(dev, stream)), "gdn2_step")
+    _launch("gdn2_step", dev, stream, ctypes.byref(args))
     return out
 
 
@@ -784,7 +809,7 @@ def mlstm_fwd(q, k, v, igate, fgate, state=None, scale=None, *, norm_weight=None
                      C_in=_p(si[0]), n_in=_p(si[1]), m_in=_p(si[2]), norm_weight=_p(norm_weight), h=_p(h),
                      C_out=_p(so[0]), n_out=_p(so[1]), m_out=_p(so[2]),
                      workspace=_status(workspace, dev))
-    _check(lib().mlstm_chunk_fwd(ctypes.byref(args), _stream(dev, stream)), "mlstm_chunk_fwd")
+    _launch("mlstm_chunk_fwd", dev, stream, ctypes.byref(args))
     return h, state_out
 
 
@@ -819,7 +844,7 @@ def mlstm_step(q, k, v, igate, fgate, state, scale=None, *, norm_weight=None, no
                          norm_eps=float(norm_eps), q=_p(q), k=_p(k), v=_p(v), igate=_p(igate), fgate=_p(fgate),
                          C=_p(state[0]), n=_p(state[1]), m=_p(state[2]), norm_weight=_p(norm_weight), h=_p(h),
                          workspace=_status(workspace, dev))
-    _check(lib().mlstm_step(ctypes.byref(args), _stream(dev, stream)), "mlstm_step")
+    _launch("mlstm_step", dev, stream, ctypes.byref(args))
     return h
 
 
@@ -839,12 +864,12 @@ class _Entry:
         packer = struct.Struct(fmt)
         self.name, self.pack, self.size, self.f = name, packer.pack, packer.size, None
 
-    def __call__(self, stream, *fields):
+    def __call__(self, device, stream, *fields):
         if self.f is None:
             f = lib()[self.name]  # a function object of its own, beside the one with typed arguments
             f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
             self.f = f
-        rc = self.f(self.pack(*fields), stream)
+        rc = _on_device(self.f, device, stream, self.pack(*fields))
         if rc:
             raise SsmError(rc, self.name)
 
@@ -859,18 +884,6 @@ _layernorm_bwd = _Entry("ssm_layernorm_bwd", _LAYERNORM + "5PN")
 _embed_fwd = _Entry("ssm_embed_fwd", "3qiifi4P")
 _embed_bwd = _Entry("ssm_embed_bwd", "4qiifi4PNP")
 _w4_matvec = _Entry("ssm_w4_matvec", "4qii6PN")
-
-
-def _raw_stream(device, stream):
-    """The address of the stream a call runs on."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(stream):
@@ -1025,7 +1038,7 @@ def glr_fwd(x, rgate, igate, lam, h0=None, *, c=8.0, return_last_state=False, sa
     if save_ckpt and ckpt is None:
         ckpt = _empty(stream, (B, (L + GLR_CKPT_INTERVAL - 1) // GLR_CKPT_INTERVAL, D), torch.float32, dev)
     fields, _keep = _glr_fields(x, rgate, igate, lam, c, h0, yp, lastp, ckpt, workspace, dev, io, code, stream)
-    _glr_fwd(_raw_stream(dev, stream), *fields)
+    _glr_fwd(dev, stream, *fields)
     return y, h_last, ckpt
 
 
@@ -1057,7 +1070,7 @@ def glr_bwd(x, rgate, igate, lam, dy, ckpt, *, c=8.0, dh_last=None, return_dh0=F
     if return_dh0 or o.get("dh0") is not None:
         o["dh0"], dhp = _out(o.get("dh0"), "dh0", stream, (B, D), f32, dev)
     fields, _keep = _glr_fields(x, rgate, igate, lam, c, None, 0, 0, ckpt, workspace, dev, io, code, stream)
-    _glr_bwd(_raw_stream(dev, stream), *fields, _at(_must(dy, "dy"), "dy", shape, io, dev),
+    _glr_bwd(dev, stream, *fields, _at(_must(dy, "dy"), "dy", shape, io, dev),
              _at(dh_last, "dh_last", (B, D), f32, dev), dxp, drp, dip, dlp, dhp)
     return o
 
@@ -1076,7 +1089,7 @@ def glr_step(state, x_t, rgate_t, igate_t, lam, *, c=8.0, y_t=None, workspace=No
     rp, rs = _rows_at(rgate_t, "rgate_t", lead, D, io, dev)
     ip, is_ = _rows_at(igate_t, "igate_t", lead, D, io, dev)
     y_t, yp = _out(y_t, "y_t", stream, shape, io, dev)
-    _glr_step(_raw_stream(dev, stream), B, D, xs, rs, is_, code, c, xp, rp, ip,
+    _glr_step(dev, stream, B, D, xs, rs, is_, code, c, xp, rp, ip,
               _at(_must(lam, "lam"), "lam", (D,), f32, dev), _at(_must(state, "state"), "state", shape, f32, dev),
               yp, _status(workspace, dev))
     return y_t
@@ -1138,7 +1151,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, save_stats=Tr
     if save_stats:
         mean, mp = _out(None, "mean", stream, lead, f32, dev)
         rstd, rp = _out(None, "rstd", stream, lead, f32, dev)
-    _layernorm_fwd(_raw_stream(dev, stream), rows, D, stride, code, eps, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
+    _layernorm_fwd(dev, stream, rows, D, stride, code, eps, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
                    _at(bias, "bias", (D,), f32, dev, 0), yp, mp, rp, _status(workspace, dev))
     return y, mean, rstd
 
@@ -1159,7 +1172,7 @@ def layer_norm_bwd(x, dy, mean, rstd, weight=None, *, dx=None, want_dweight=True
     db, dbp = _out(None, "dbias", stream, (D,), f32, dev) if want_dbias else (None, 0)
     n = layer_norm_workspace_bytes(rows, D) if want_dweight or want_dbias else 0
     _part, partp = _out(None, "partial sums", stream, (n,), torch.uint8, dev) if n else (None, 0)
-    _layernorm_bwd(_raw_stream(dev, stream), rows, D, stride, code, 0.0, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
+    _layernorm_bwd(dev, stream, rows, D, stride, code, 0.0, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
                    0, 0, _at(_must(mean, "mean"), "mean", lead, f32, dev, 0), _at(_must(rstd, "rstd"), "rstd", lead, f32, dev, 0),
                    _status(workspace, dev), _at(_must(dy, "dy"), "dy", shape, io, dev, 0), dxp, dwp, dbp, partp, n)
     return {"dx": dx, "dweight": dw, "dbias": db}
@@ -1195,7 +1208,7 @@ def embed_fwd(ids, weight, scale=1.0, *, out=None, workspace=None, stream=None):
     V, D = weight.shape
     shape = ids.shape + (D,)
     out, outp = _out(out, "out", stream, shape, io, dev, 0)
-    _embed_fwd(_raw_stream(dev, stream), ids.numel(), V, D, code, ids64, scale, 0, ids.data_ptr(),
+    _embed_fwd(dev, stream, ids.numel(), V, D, code, ids64, scale, 0, ids.data_ptr(),
                _at(weight, "weight", (V, D), io, dev, 0), outp, _status(workspace, dev))
     return out
 
@@ -1221,7 +1234,7 @@ def embed_bwd(ids, dy, V, scale=1.0, *, padding_idx=None, dweight=None, workspac
     dweight, dwp = _out(dweight, "dweight", stream, (V, D), torch.float32, dev, 0)
     n = embed_workspace_bytes(tokens, V, D)
     _ws, wsp = _out(None, "scratch", stream, (n,), torch.uint8, dev) if n else (None, 0)
-    _embed_bwd(_raw_stream(dev, stream), tokens, V, D, pad, code, ids64, scale, 0, ids.data_ptr(),
+    _embed_bwd(dev, stream, tokens, V, D, pad, code, ids64, scale, 0, ids.data_ptr(),
                _at(dy, "dy", ids.shape + (D,), io, dev, 0), dwp, wsp, n, _status(workspace, dev))
     return dweight
 
@@ -1248,7 +1261,7 @@ def w4_quantize(w, group=128, *, stream=None):
     with _on(stream):
         q = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
         s = torch.empty((N, K // group), dtype=torch.bfloat16, device=dev)
-    _check(lib().ssm_w4_quantize(N, K, group, _IO[w.dtype], _p(w), _p(q), _p(s), _stream(dev, stream)), "ssm_w4_quantize")
+    _launch("ssm_w4_quantize", dev, stream, N, K, group, _IO[w.dtype], _p(w), _p(q), _p(s))
     return q, s
 
 
@@ -1288,7 +1301,7 @@ def w4_matvec(x, qweight, scales, bias=None, *, out_dtype=torch.bfloat16, out=No
     elif n > 256:  # (256 bytes hold only the status, which nobody asked for)
         keep = _empty(stream, n, torch.uint8, dev)
         wp = keep.data_ptr()
-    _w4_matvec(_raw_stream(dev, stream), M, N, K, stride, group, code, xp, _at(qweight, "qweight", (N, K // 2), torch.uint8, dev),
+    _w4_matvec(dev, stream, M, N, K, stride, group, code, xp, _at(qweight, "qweight", (N, K // 2), torch.uint8, dev),
                _at(scales, "scales", (N, groups), bf, dev, 0), _at(bias, "bias", (N,), torch.float32, dev, 0), outp, wp, n)
     return out
 
@@ -1300,7 +1313,7 @@ def exp2_fma(x, *, out=None, stream=None):
         raise TypeError("x must be a contiguous fp32 CUDA tensor")
     out = torch.empty_like(x) if out is None else out
     _need(out, "out", tuple(x.shape), torch.float32, x.device)
-    _check(lib().ssm_exp2_fma(_p(x), _p(out), x.numel(), _stream(x.device, stream)), "ssm_exp2_fma")
+    _launch("ssm_exp2_fma", x.device, stream, _p(x), _p(out), x.numel())
     return out
 
 
@@ -1308,12 +1321,12 @@ def poll_status(workspace, stream=None) -> int:
     """Synchronise, read and clear the status word. 0 = ok, -7 = non-finite output seen, -6 = a bounded
     wait inside a kernel ran out."""
     dev = workspace.buf.device
-    return int(lib().ssm_poll_status(workspace.buf.data_ptr(), _stream(dev, stream)))
+    return int(_on_device(lib().ssm_poll_status, dev, stream, workspace.buf.data_ptr()))
 
 
 def clear_status(workspace, stream=None) -> None:
     dev = workspace.buf.device
-    _check(lib().ssm_clear_status(workspace.buf.data_ptr(), _stream(dev, stream)), "ssm_clear_status")
+    _launch("ssm_clear_status", dev, stream, workspace.buf.data_ptr())
 
 
 class HostPipeline:
