@@ -957,6 +957,9 @@ def _short_way():
     if _short is None:
         h = lib()
         try:
+            from . import _builder
+            if not _builder.binding_fits():
+                raise ImportError("_binding.so is not there, or was built for another torch or Python")
             from . import _binding
             _binding.bind(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value for n in _SHORT_ENTRIES))
             _short = _binding

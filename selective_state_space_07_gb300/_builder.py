@@ -39,16 +39,30 @@ def nvcc() -> str:
 
 
 BINDING = os.path.join(HERE, "_binding.so")
-BINDING_TORCH = os.path.join(BUILD, "binding_torch.txt")  # the torch that _binding.so was built against
+BINDING_TORCH = os.path.join(BUILD, "binding_torch.txt")  # what _binding.so was built for
 
 
 def _binding_inputs():
     return [os.path.join(CSRC, "binding.cpp"), os.path.abspath(__file__)] + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
-def binding_stale() -> bool:
+def _binding_tag() -> str:
+    """The torch and the Python that run: whose C++ and C interfaces _binding.so uses."""
     import torch
-    if not os.path.exists(BINDING) or not os.path.exists(BINDING_TORCH) or open(BINDING_TORCH).read() != torch.__version__:
+    return f"torch {torch.__version__} {torch._C._GLIBCXX_USE_CXX11_ABI} {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_fits() -> bool:
+    """Whether _binding.so is there and was built for this torch and this Python: only then may it be loaded."""
+    try:
+        with open(BINDING_TORCH) as f:
+            return os.path.exists(BINDING) and f.read() == _binding_tag()
+    except OSError:
+        return False
+
+
+def binding_stale() -> bool:
+    if not binding_fits():
         return True
     t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(p) > t for p in _binding_inputs())
@@ -71,9 +85,11 @@ def _build_binding() -> None:
             os.remove(BINDING)
         warnings.warn(f"_binding.so was not built; the ctypes binding makes its calls:\n{r.stdout[-2000:]}\n{r.stderr[-2000:]}")
         return
+    if os.path.exists(BINDING_TORCH):
+        os.remove(BINDING_TORCH)  # (so that it never speaks of another file than the one that lies there)
     os.replace(tmp, BINDING)
     with open(BINDING_TORCH, "w") as f:
-        f.write(torch.__version__)
+        f.write(_binding_tag())
 
 
 def _inputs():

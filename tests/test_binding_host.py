@@ -139,3 +139,22 @@ def test_a_stream_of_another_device_is_refused(ssm, two_gpus):
 def test_no_cuda_device(ssm):
     with pytest.raises(ValueError, match="CUDA"):
         ssm.poll_status(ssm.Workspace.of_bytes(256, "cpu"))
+
+
+@pytest.mark.parametrize("built_for", [None, "torch 1.0.0 True cpython-312-x86_64-linux-gnu", "2.0.1"])
+def test_a_short_way_built_for_another_torch_is_not_loaded(ssm, monkeypatch, tmp_path, built_for):
+    from selective_state_space_07_gb300 import _builder
+    note = tmp_path / "built_for.txt"
+    if built_for is not None:
+        note.write_text(built_for)
+    monkeypatch.setattr(_builder, "BINDING_TORCH", str(note))
+    monkeypatch.setattr(ssm, "_short", None)
+    assert not ssm._short_way() and _builder.binding_stale()
+
+
+def test_the_short_way_that_build_made_is_loaded(ssm, monkeypatch):
+    from selective_state_space_07_gb300 import _builder
+    if not _builder.binding_fits():
+        pytest.skip("the short way was not built here")
+    monkeypatch.setattr(ssm, "_short", None)
+    assert ssm._short_way() is ssm._binding and not _builder.binding_stale()
