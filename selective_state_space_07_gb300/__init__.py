@@ -1220,20 +1220,20 @@ def embed_bwd(ids, dy, V, scale=1.0, *, padding_idx=None, dweight=None, workspac
     """Gradient of embed_fwd's table: dweight[v] = scale * sum of dy over the tokens with ids == v, [V, D] fp32, every
     row written (zeros where no token names it, and for ``padding_idx``); the tokens sorted by id and summed in their
     order, the same bits every time. dy [..., D] fp32 or bf16. ``workspace`` takes the status word."""
+    pad = -1  # (none)
+    if padding_idx is not None:
+        pad = int(padding_idx)
+        if not 0 <= pad < V:
+            raise ValueError(f"padding_idx {pad} is outside [0, {V})")
     if stream is None and (_short or _short_way()):
-        r = _short.embed_bwd(ids, dy, V, scale, -1 if padding_idx is None else padding_idx, dweight, _buf(workspace))
-        if r is not None and (padding_idx is None or padding_idx >= 0):
+        r = _short.embed_bwd(ids, dy, V, scale, pad, dweight, _buf(workspace))
+        if r is not None:
             return r
     dev, ids64 = _ids(ids)
     _, io, code = _io_of(dy, "dy", None, "the embedding")
     if dy.dim() < 1:
         raise ValueError("dy must be [..., D]")
     D, tokens = dy.shape[-1], ids.numel()
-    pad = -1
-    if padding_idx is not None:
-        pad = int(padding_idx)
-        if not 0 <= pad < V:
-            raise ValueError(f"padding_idx {pad} is outside [0, {V})")
     dweight, dwp = _out(dweight, "dweight", stream, (V, D), torch.float32, dev, 0)
     n = embed_workspace_bytes(tokens, V, D)
     _ws, wsp = _out(None, "scratch", stream, (n,), torch.uint8, dev) if n else (None, 0)

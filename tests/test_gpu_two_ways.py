@@ -86,3 +86,11 @@ def test_a_workspace_on_the_same_device_is_used(ssm, way):
     bad = torch.tensor([1, -1, 3, 0], device="cuda")
     ssm.embed_fwd(bad, torch.randn(4, 64, device="cuda"), workspace=ws)
     assert ssm.poll_status(ws) == -9
+
+
+@pytest.mark.parametrize("pad", [-1, -2, 9, 10])
+def test_a_wrong_padding_index_is_refused_before_anything_is_written(ssm, way, pad):
+    dw = torch.full((9, 64), 7.0, device="cuda")
+    with pytest.raises(ValueError, match="padding_idx"):
+        ssm.embed_bwd(torch.tensor([1, 2], device="cuda"), torch.ones(2, 64, device="cuda"), 9, padding_idx=pad, dweight=dw)
+    assert bool((dw == 7.0).all())
