@@ -14,7 +14,7 @@
  * An id outside [0, V) reads nothing: its output row is zero, its gradient
  * row goes nowhere, and the status word says so (ssm_poll_status:
  * SSM_ERR_INDEX). padding_id takes part in the lookup like any id; its
- * gradient is zero. padding_id < 0: none.
+ * gradient is zero. padding_id outside [0, V): none.
  *
  * Any D >= 1, any alignment of W, out, dy and dW that suits their elements
  * (else SSM_ERR_ALIGNMENT); rows whose starts are not all on 16 bytes are read

@@ -568,7 +568,7 @@ int ssm_embed_bwd(const ssm_embed_bwd_args* a, void* stream) {
         using ID = decltype(tag);
         static unsigned long long all_mask = 0, part_mask = 0, divide_mask = 0;
         const ssm::AllTokens<ID> all{static_cast<const ID*>(a->ids), (int)a->tokens, (unsigned)a->V,
-                                     a->padding_id < 0 ? ssm::kNoId : (unsigned)a->padding_id};
+                                     a->padding_id < 0 || a->padding_id >= a->V ? ssm::kNoId : (unsigned)a->padding_id};
         unsigned* status = static_cast<unsigned*>(a->status);
         if (a->tokens <= ssm::kDirect || grid > (unsigned)ssm::kMostRanges) {
             if (!ssm::ensure_smem(ssm::embed_sort_kernel<ssm::AllTokens<ID>>, most, all_mask)) return -1;
