@@ -33,7 +33,8 @@
  * non-null (else SSM_ERR_INVALID_ARG); at most 2^31 - 65 token rows and 2^31 - 1
  * tiles of 32 tokens x 64 channels (else SSM_ERR_UNSUPPORTED). B, L or D may be 0; with L = 0
  * h_last is h0, dh0 is dh_last and dlam is zero. Outputs must not overlap
- * inputs, except that dx may be dy.
+ * inputs, except that dx may be dy, h_last h0 and dh0 dh_last (the state is
+ * then carried on in its place).
  *
  * workspace: >= ssm_glr_workspace_bytes(B, L, D) bytes, 16-byte aligned: the
  * status word (ssm_poll_status: non-finite outputs; SSM_ERR_TIMEOUT if a

@@ -1027,7 +1027,7 @@ def glr_fwd(x, rgate, igate, lam, h0=None, *, c=8.0, return_last_state=False, sa
     bf16 (one dtype), each dense or a column slice of a wider [B, L, W] buffer; lam [D], h0 [B, D] fp32; D a multiple
     of 8. ``ckpt`` (what glr_bwd needs) is written unless ``save_ckpt`` is False. ``workspace`` (``glr_workspace``)
     holds the status word for poll_status; without one the call uses scratch of its own and reports no status.
-    Returns (y, h_last or None, ckpt or None)."""
+    ``h_last`` may be ``h0`` itself: the state is then carried on in place. Returns (y, h_last or None, ckpt or None)."""
     if stream is None and ckpt is None and (_short or _short_way()):
         r = _short.glr_fwd(x, rgate, igate, lam, c, h0, y, h_last, None, return_last_state, save_ckpt, _buf(workspace))
         if r is not None:
@@ -1049,7 +1049,7 @@ def glr_bwd(x, rgate, igate, lam, dy, ckpt, *, c=8.0, dh_last=None, return_dh0=F
             out: Optional[Dict] = None, workspace=None, stream=None) -> Dict[str, torch.Tensor]:
     """Backward of glr_fwd for loss = <dy, y> + <dh_last, h_last>, from the checkpoints glr_fwd saved (they hold h0 as
     well). Returns a dict with dx, drgate, digate [B, L, D] in x's dtype, dlam [D] fp32 and, if asked, dh0 [B, D] fp32.
-    ``inplace`` writes dx into dy."""
+    ``inplace`` writes dx into dy; ``out`` may hold buffers for them, dh_last itself as dh0 too."""
     if stream is None and not inplace and not out and (_short or _short_way()):
         r = _short.glr_bwd(x, rgate, igate, lam, c, dy, ckpt, dh_last, return_dh0, _buf(workspace))
         if r is not None:

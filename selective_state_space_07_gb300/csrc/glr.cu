@@ -92,6 +92,7 @@ struct GlrParams {
     float4* blocks;     // [blocks * columns, 32]: the maps of whole blocks
     float2* states;     // [spans * columns, 32]: the states behind them
     float* cs;          // [D]: c * softplus(lam)
+    float* held;        // [B, D]: a copy of start, where end is written in its place
     unsigned columns, chunks, per_row;  // columns = B * per_row
     int64_t fault_chunk1;
     unsigned long long wait_ns;
@@ -106,7 +107,7 @@ struct GlrBoxes {
 // one piece that starts as all ones. For the larger of the two tile counts
 // (fp32's), so that one size serves both types.
 struct GlrWs {
-    size_t sync, publish_bytes, maps, blocks, states, cs, part, total;
+    size_t sync, publish_bytes, maps, blocks, states, cs, held, part, total;
 };
 GlrWs glr_ws(int64_t B, int64_t L, int64_t D, int chunk) {
     const size_t columns = (size_t)B * ((D + kCols - 1) / kCols), chunks = (size_t)((L + chunk - 1) / chunk);
@@ -120,7 +121,8 @@ GlrWs glr_ws(int64_t B, int64_t L, int64_t D, int chunk) {
     w.states = w.blocks + (multi ? blocks * columns * 32 * sizeof(float4) : 0);
     w.cs = w.states + (multi ? blocks * columns * 32 * sizeof(float2) : 0);
     w.publish_bytes = w.cs - w.sync;
-    w.part = w.cs + (multi ? up((size_t)D * sizeof(float)) : 0);
+    w.held = w.cs + (multi ? up((size_t)D * sizeof(float)) : 0);
+    w.part = w.held + (multi ? up((size_t)B * D * sizeof(float)) : 0);
     w.total = w.part + up((size_t)B * chunks * D * sizeof(float));
     return w;
 }
@@ -539,6 +541,10 @@ __device__ __forceinline__ float2 finish_backward(const GlrParams& p, const Tile
 __device__ __forceinline__ float2 ldg2(const float* p, bool live) {
     return p && live ? __ldg(reinterpret_cast<const float2*>(p)) : dup(0.f);
 }
+// ... of p.start, by a kernel that may write p.end in its place behind a barrier.
+__device__ __forceinline__ float2 ld_start(const GlrParams& p, const Tile& t, int ch, bool live) {
+    return p.start && live ? *reinterpret_cast<const float2*>(p.start + t.state + ch) : dup(0.f);
+}
 
 // ---------------------------------------------------------------- one chunk
 // A sequence of at most one tile: one CTA a column, no carries, inputs
@@ -575,7 +581,7 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) glr_fwd_short
     rg.load(p.r, p.sr, p.L, t, at, nt);
     ig.load(p.i, p.si, p.L, t, at, nt);
     x.load(p.x, p.sx, p.L, t, at, nt);
-    float2 carry = ldg2(p.start ? p.start + t.state + at.ch : nullptr, at.live(p, t));
+    float2 carry = ld_start(p, t, at.ch, at.live(p, t));
     const float2 cs = own_cs(p, css, t.c0);
     float2 h[kTok<IO>], pr[kTok<IO>];
     run[warp][lane] = run_forward<IO, false>(
@@ -600,7 +606,7 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) glr_bwd_short
     ig.load(p.i, p.si, p.L, t, at, nt);
     x.load(p.x, p.sx, p.L, t, at, nt);
     dy.load(p.dy, p.D, p.L, t, at, nt);
-    float2 h = ldg2(p.ckpt + t.saved + at.ch, live), v = ldg2(p.start ? p.start + t.state + at.ch : nullptr, live);
+    float2 h = ldg2(p.ckpt + t.saved + at.ch, live), v = ld_start(p, t, at.ch, live);
     const float2 cs = own_cs(p, css, t.c0);
     float2 w[kTok<IO>], r[kTok<IO>], i[kTok<IO>], back, sum;
     maps.run[warp][lane] = run_backward<IO, false>(
@@ -630,15 +636,19 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) glr_bwd_short
 }
 
 // ---------------------------------------------------------------- many chunks
-// Sets the published words to empty and c * softplus(lam) down for the tiles.
+// Sets the published words to empty and c * softplus(lam) down for the tiles;
+// and copies the start (held: nullable) where the end is written over it: a
+// tile of the first span may read it after the last tile has written that.
 __global__ void __launch_bounds__(256) glr_prepare_kernel(uint4* publish, int64_t n16, const float* __restrict__ lam,
-                                                        float c, float* cs, int64_t D) {
+                                                        float c, float* cs, int64_t D, const float* start, float* held, int64_t states) {
     begin_kernel();
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < n16; j += step)
         publish[j] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
     for (int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < D; j += step)
         cs[j] = c * softplus_full(__ldg(lam + j));
+    if (!held) return;
+    for (int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < states; j += step) held[j] = start[j];
 }
 
 // The ring of staged tiles of a CTA. A stage holds a tile's boxes of rgate,
@@ -994,6 +1004,7 @@ GlrParams base_params(const ssm_glr_args& a) {
     p.blocks = reinterpret_cast<float4*>(ws + w.blocks);
     p.states = reinterpret_cast<float2*>(ws + w.states);
     p.cs = reinterpret_cast<float*>(ws + w.cs);
+    p.held = reinterpret_cast<float*>(ws + w.held);
     p.part = reinterpret_cast<float*>(ws + w.part);
     p.chunks = (unsigned)((a.L + chunk - 1) / chunk);
     p.per_row = (unsigned)((a.D + kCols - 1) / kCols);
@@ -1028,7 +1039,7 @@ template <typename IO> bool encode_boxes(const GlrParams& p, bool bwd, GlrBoxes&
     return enc(&bx.x, p.x, p.sx) && enc(&bx.r, p.r, p.sr) && enc(&bx.i, p.i, p.si) && (!bwd || enc(&bx.dy, p.dy, p.D));
 }
 
-template <typename IO> int launch_seq(bool bwd, const GlrParams& p, size_t publish_bytes, cudaStream_t s) {
+template <typename IO> int launch_seq(bool bwd, GlrParams p, size_t publish_bytes, cudaStream_t s) {
     if (p.chunks == 1) {
         return launch_next(bwd ? glr_bwd_short_kernel<IO> : glr_fwd_short_kernel<IO>, dim3(p.columns), kThreads, 0, s, p);
     }
@@ -1036,9 +1047,11 @@ template <typename IO> int launch_seq(bool bwd, const GlrParams& p, size_t publi
     if (!encode_boxes<IO>(p, bwd, bx)) return -1;
     const int64_t n16 = (int64_t)(publish_bytes / 16), want = (n16 + 1023) / 1024 + (p.D + 255) / 256;
     const int64_t cap = 8 * (int64_t)sm_count();
+    const bool in_place = p.start && p.start == p.end;
     if (launch_next(glr_prepare_kernel, dim3((unsigned)(want < cap ? want : cap)), 256, 0, s, reinterpret_cast<uint4*>(p.sync), n16,
-                    p.lam, p.c, p.cs, p.D) < 0)
+                    p.lam, p.c, p.cs, p.D, p.start, in_place ? p.held : nullptr, p.B * p.D) < 0)
         return -1;
+    if (in_place) p.start = p.held;
     const bool few = p.columns <= kFewColumns && p.chunks > kBlock;
     constexpr int kFwdSmem = Ring<IO, 3, kFwdStages>::kSmem, kBwdSmem = Ring<IO, 4, kBwdStages>::kSmem;
     int r;
