@@ -83,9 +83,9 @@ __device__ __forceinline__ unsigned two_weights(unsigned v) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x43084308u));  // 136
     return r;
 }
-// A unit's scales of one row: bf16 pairs, for G groups from s on; groups past
-// the last, the `left` th, are that one again (x is zero there). The loads stay
-// in front of the waits that follow them.
+// A unit's scales of one row: bf16 pairs, for G groups from s on; zero for
+// groups past the last, the `left` th (x is zero there, too, and an infinite
+// scale must not meet it). The loads stay in front of the waits that follow them.
 template <int G> struct Scales {
     unsigned v[G / 2];
     __device__ __forceinline__ void load(bool wide, const unsigned short* s, int left) {
@@ -96,7 +96,7 @@ template <int G> struct Scales {
         } else {
 #pragma unroll
             for (int j = 0; j < G; j += 2)
-                v[j / 2] = __ldg(s + min(j, left - 1)) | (unsigned)__ldg(s + min(j + 1, left - 1)) << 16;
+                v[j / 2] = (j < left ? __ldg(s + j) : 0u) | (j + 1 < left ? (unsigned)__ldg(s + j + 1) : 0u) << 16;
         }
     }
     __device__ __forceinline__ float get(int j) const {
