@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(T* R) ln_bwd_kernel(const LnParams p) {
         for (int k = 0; k < NC; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                // elements past the row are 0 in g and so take no part, whatever xh is there
-                xh[k][i] = (xh[k][i] - m) * rs;
+                // elements past the row are 0 in g, and in xh, too: -m rs could be infinite
+                xh[k][i] = column<L, T>((int64_t)k * 8 * T, t, i) < p.D ? (xh[k][i] - m) * rs : 0.f;
                 dw[k][i] = __fmaf_rn(g[k][i], xh[k][i], dw[k][i]);
                 db[k][i] += g[k][i];
                 g[k][i] *= w[k][i];
@@ -390,6 +390,29 @@ template <typename IO, Layout L, int T> __device__ __forceinline__ void take_pai
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
 }
+// The same with `fill` past the row, but where rows are read in eights.
+template <typename IO, Layout L, int T>
+__device__ __forceinline__ void take_pairs(const IO* row, int D, int c0, int t, IO fill, float2 (&v)[4]) {
+    if constexpr (L == Layout::kOct) {
+        take_pairs<IO, L, T>(row, D, c0, t, v);
+    } else {
+        Chunk<IO, L, T> in;
+        in.take(row, D, c0, t, fill);
+        float f[8];
+        in.get(f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pk(f[2 * i], f[2 * i + 1]);
+    }
+}
+// ... and normalised, (x + c) a. What has passed the row must be finite there, also where c a is not (a row of equal
+// elements far from zero): it is read as -c, rounded to the row's type (equal elements are of that type), or a taken as 0.
+template <typename IO, Layout L, int T>
+__device__ __forceinline__ void take_normalised(const IO* row, int D, int c0, int t, float2 c, float2 a, IO fill, float2 (&v)[4]) {
+    take_pairs<IO, L, T>(row, D, c0, t, fill, v);
+    if (L == Layout::kOct && c0 + 8 * t >= D) a = pk(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(__fadd2_rn(v[i], c), a);
+}
 template <typename IO, Layout L, int T> __device__ __forceinline__ void store_pairs(IO* row, int64_t D, int c0, int t, const float2 (&v)[4]) {
     const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
     Chunk<IO, L, T>::store(row, D, c0, t, f);
@@ -518,6 +541,7 @@ __global__ void __launch_bounds__(T* R, 1) ln_bwd_ring_kernel(const LnParams p) 
     IO* to = static_cast<IO*>(p.dx) + row0 * p.D;
     for (int64_t row = row0; row < p.rows; row += feed.step, to += feed.step * p.D) {
         const float2 a = splat(rstd), c = splat(-mean);
+        const IO fill = IOT<IO>::from_f(mean), zero = IOT<IO>::from_f(0.f);
         mp += feed.step, rp += feed.step;
         if (row + feed.step < p.rows) mean = __ldg(mp), rstd = __ldg(rp);
         feed.wait();
@@ -526,18 +550,17 @@ __global__ void __launch_bounds__(T* R, 1) ln_bwd_ring_kernel(const LnParams p) 
         float2 s0 = pk(0.f, 0.f), s1 = pk(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            float2 xv[4], g[4], wk[4];
-            take_pairs<IO, L, T>(x, D, k * 8 * T, t, xv);
-            take_pairs<IO, L, T>(dy, D, k * 8 * T, t, g);  // (what lies past the row is 0 here and so takes no part)
+            float2 xh[4], g[4], wk[4];
+            take_normalised<IO, L, T>(x, D, k * 8 * T, t, c, a, fill, xh);
+            take_pairs<IO, L, T>(dy, D, k * 8 * T, t, zero, g);  // (so what lies past the row takes no part)
             column_pairs<T>(w, k, t, wk);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 xh = __fmul2_rn(__fadd2_rn(xv[i], c), a);
-                dw[k][i] = __ffma2_rn(g[i], xh, dw[k][i]);
+                dw[k][i] = __ffma2_rn(g[i], xh[i], dw[k][i]);
                 db[k][i] = __fadd2_rn(db[k][i], g[i]);
                 const float2 h = __fmul2_rn(g[i], wk[i]);
                 s0 = __fadd2_rn(s0, h);
-                s1 = __ffma2_rn(h, xh, s1);
+                s1 = __ffma2_rn(h, xh[i], s1);
             }
         }
         const float2 s = group_sum2<T, R>(sh, turn++, group, t, s0.x + s0.y, s1.x + s1.y);
@@ -546,14 +569,13 @@ __global__ void __launch_bounds__(T* R, 1) ln_bwd_ring_kernel(const LnParams p) 
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
             if (k * 8 * T >= D) break;
-            float2 xv[4], g[4], wk[4];
-            take_pairs<IO, L, T>(x, D, k * 8 * T, t, xv);
-            take_pairs<IO, L, T>(dy, D, k * 8 * T, t, g);
+            float2 xh[4], g[4], wk[4];
+            take_normalised<IO, L, T>(x, D, k * 8 * T, t, c, a, fill, xh);
+            take_pairs<IO, L, T>(dy, D, k * 8 * T, t, zero, g);
             column_pairs<T>(w, k, t, wk);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 xh = __fmul2_rn(__fadd2_rn(xv[i], c), a);
-                g[i] = __ffma2_rn(__fmul2_rn(g[i], wk[i]), a, __ffma2_rn(xh, c2, c1));
+                g[i] = __ffma2_rn(__fmul2_rn(g[i], wk[i]), a, __ffma2_rn(xh[i], c2, c1));
                 bad = __ffma2_rn(g[i], splat(0.f), bad);
             }
             store_pairs<IO, L, T>(to, p.D, k * 8 * T, t, g);
@@ -684,7 +706,7 @@ template <typename IO, Layout L> __global__ void __launch_bounds__(kWideThreads)
                 const int64_t c = column<L, T>(c0, t, i);
                 const float h = g[i] * (p.w && c < p.D ? __ldg(p.w + c) : 1.f);
                 s0 += h;
-                s1 = __fmaf_rn(h, (v[i] - mean) * rstd, s1);
+                if (c < p.D) s1 = __fmaf_rn(h, (v[i] - mean) * rstd, s1);
             }
         }
         const float c1 = cta_sum(s0, sh) * p.inv_d, c2 = cta_sum(s1, sh) * p.inv_d;

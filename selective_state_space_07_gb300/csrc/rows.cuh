@@ -30,8 +30,9 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
 }
 
 // A thread's eight elements of the chunk that starts at column c0 of a row of
-// D; elements from D on read as zero and are not written. load reads global
-// memory, take a row in shared memory (or, element by element, either).
+// D; elements from D on read as zero (by the second form of take as `fill`) and
+// are not written. load reads global memory, take a row in shared memory (or,
+// element by element, either).
 template <typename IO, Layout L, int T> struct Chunk;
 template <int T> struct Chunk<__nv_bfloat16, Layout::kOct, T> {
     uint4 v;
@@ -81,6 +82,13 @@ template <int T> struct Chunk<float, Layout::kQuad, T> {
             v[i] = e < D ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
+    __device__ __forceinline__ void take(const float* row, int D, int c0, int t, float fill) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = c0 + 4 * t + 4 * T * i;
+            v[i] = e < D ? *reinterpret_cast<const float4*>(row + e) : make_float4(fill, fill, fill, fill);
+        }
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) f[4 * i] = v[i].x, f[4 * i + 1] = v[i].y, f[4 * i + 2] = v[i].z, f[4 * i + 3] = v[i].w;
@@ -123,6 +131,12 @@ template <typename IO, int T> struct Chunk<IO, Layout::kEach, T> {
         for (int i = 0; i < 8; ++i) v[i] = i * T < left ? q[i * T] : IOT<IO>::from_f(0.f);
     }
     __device__ __forceinline__ void take(const IO* row, int D, int c0, int t) { load(row, D, c0, t); }
+    __device__ __forceinline__ void take(const IO* row, int D, int c0, int t, IO fill) {
+        const IO* q = row + c0 + t;
+        const int left = (int)min64((int64_t)D - c0 - t, 8 * T);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i * T < left ? q[i * T] : fill;
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = IOT<IO>::to_f(v[i]);
