@@ -16,7 +16,8 @@
  * from the centred values (no cancellation for rows with a large mean).
  * Summing orders are fixed: the same inputs give the same bits.
  *
- * rows or D may be 0 (dw, db are then zero). eps finite and non-negative,
+ * rows or D may be 0 (dw, db are then zero; mean and rstd of rows without
+ * elements are not written). eps finite and non-negative,
  * sizes non-negative, x_stride 0 or >= D (else SSM_ERR_INVALID_ARG). y may be
  * x, and dx may be dy or x, where those are dense; nothing else may overlap.
  * status: nullable, >= 256 bytes, 16-byte aligned: the status word

@@ -1141,7 +1141,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, save_stats=Tr
     """Layer norm over the last axis (C ABI in ``include/layernorm.h``): y = (x - mean) * rstd * weight + bias, rstd =
     1/sqrt(var + eps). x [..., D] fp32 or bf16, dense or with evenly spaced rows (a column slice); weight, bias [D] fp32
     or None. Returns (y, mean, rstd): y dense in x's dtype, mean and rstd [...] fp32 for layer_norm_bwd (None unless
-    ``save_stats``). ``workspace`` takes the status word for poll_status."""
+    ``save_stats``; NaN where D is 0). ``workspace`` takes the status word for poll_status."""
     if stream is None and (_short or _short_way()):
         r = _short.layer_norm_fwd(x, weight, bias, eps, y, save_stats, _buf(workspace))
         if r is not None:
@@ -1154,6 +1154,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, save_stats=Tr
     if save_stats:
         mean, mp = _out(None, "mean", stream, lead, f32, dev)
         rstd, rp = _out(None, "rstd", stream, lead, f32, dev)
+        if D == 0:  # rows without elements: 0 / 0
+            with _on(stream):
+                mean.fill_(float("nan")), rstd.fill_(float("nan"))
     _layernorm_fwd(dev, stream, rows, D, stride, code, eps, x.data_ptr(), _at(weight, "weight", (D,), f32, dev, 0),
                    _at(bias, "bias", (D,), f32, dev, 0), yp, mp, rp, _status(workspace, dev))
     return y, mean, rstd
