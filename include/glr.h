@@ -116,11 +116,11 @@ size_t ssm_glr_workspace_bytes(int64_t B, int64_t L, int64_t D);
 /* fp32 elements of the checkpoint buffer: B * ceil(L/32) * D. */
 int64_t ssm_glr_ckpt_elems(int64_t B, int64_t L, int64_t D);
 
-/* Test hook: arms, for this thread's next ssm_glr_fwd only, a missing carry:
+/* Test hook: arms, for this thread's next ssm_glr_fwd or ssm_glr_bwd only, a missing carry:
  * the tiles of chunk `chunk` (64 tokens in bf16, 32 in fp32, counted from 0) withhold what they
  * would hand on, and every bounded wait of that call gives up after wait_ns
- * (0: one second). The tiles behind it stop and ssm_poll_status returns
- * SSM_ERR_TIMEOUT. chunk < 0 disarms. SSM_ERR_INVALID_ARG for wait_ns above
+ * (0: one second). The tiles that come after it in the scan (in the backward the
+ * earlier chunks) stop and ssm_poll_status returns SSM_ERR_TIMEOUT. chunk < 0 disarms. SSM_ERR_INVALID_ARG for wait_ns above
  * 10 s. */
 int ssm_glr_debug_arm_wait_fault(int64_t chunk, uint64_t wait_ns);
 

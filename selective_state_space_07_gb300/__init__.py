@@ -1099,7 +1099,7 @@ def glr_step(state, x_t, rgate_t, igate_t, lam, *, c=8.0, y_t=None, workspace=No
 
 
 def glr_arm_wait_fault(chunk: int, wait_ns: int) -> None:
-    """Test hook: in the next glr_fwd of this thread the tiles of chunk `chunk` withhold their carry and every wait is
+    """Test hook: in the next glr_fwd or glr_bwd of this thread the tiles of chunk `chunk` withhold their carry and every wait is
     bounded by wait_ns, so the call ends with SSM_ERR_TIMEOUT in the status word. chunk < 0 disarms."""
     _check(lib().ssm_glr_debug_arm_wait_fault(int(chunk), int(wait_ns)), "ssm_glr_debug_arm_wait_fault")
 

@@ -38,9 +38,9 @@
 //
 // Measured, bf16 unless said, in percent of the HBM copy rate, for slow decays
 // (c softplus(lam) < 1/4): 4 x 4096 x 4096 forward with checkpoints 101 us
-// (79%), backward 208 (67%), other decays 108 and 230; 4 x 2048 x 4096 fp32 90
-// (87%) and 159 (87%). 1 x 65536 x 2048: 267 us (59%) and 520, other decays 281
-// and 600; each of its 19 chunks at work at a time waits for those before it.
+// (79%), backward 200 (69%), other decays 108 and 223; 4 x 2048 x 4096 fp32 89
+// (88%) and 157 (88%). 1 x 65536 x 2048: 267 us (59%) and 481, other decays 281
+// and 553; each of its 19 chunks at work at a time waits for those before it.
 // Registers allow 16 warps an SM forward and 12 backward, which issue in half
 // of the slots (32 and 59 instructions an element). 2 x 509 x 256 fp32, both
 // passes 22 us: launches.
@@ -249,8 +249,8 @@ template <bool SERIES> __device__ __forceinline__ Held held_decay(float2 v) {
     return {n, __ffma2_rn(v, dup(-1.f), n)};
 }
 // Whether the series is enough for all of a warp's channels. (It alone: 101 us
-// forward, 208 backward at 4 x 4096 x 4096 bf16; with the choice for each
-// element 108 and 230.)
+// forward, 200 backward at 4 x 4096 x 4096 bf16; with the choice for each
+// element 108 and 223.)
 __device__ __forceinline__ bool all_series(float2 cs) { return __all_sync(0xffffffffu, cs.x < 0.25f && cs.y < 0.25f); }
 // 1 - a^2 of w = 1 - a
 __device__ __forceinline__ float2 input_power(float2 w) { return __fmul2_rn(w, __ffma2_rn(w, dup(-1.f), dup(2.f))); }
@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) glr_bwd_kernel(const GlrPa
         float2 sum;
         // A body for each way to the decays (the warps of a CTA have the same channels, and so take the same one): with
         // one for both, or with the input gates kept outside the series too, registers spill (4 x 4096 x 4096 bf16:
-        // 208 us in the series and 230 outside, otherwise 250 to 320).
+        // 200 us in the series and 223 outside, otherwise 250 to 320).
         auto work = [&](auto way) {
             constexpr bool SERIES = decltype(way)::value;
             float2 w[T], r[T], i[T], back;
@@ -843,14 +843,15 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) glr_bwd_kernel(const GlrPa
                 }
             }
             const float4 whole = compose(behind, make_float4(mine.x, mine.y, back.x, back.y));  // warp 0: the tile's map
-            if (warp == 0) publish_map(p, t, whole);
+            const bool publishes = warp == 0 && p.fault_chunk1 != (int64_t)t.chunk + 1;
+            if (publishes) publish_map(p, t, whole);
 #pragma unroll
             for (int u = 0; u < kWarps - 1; ++u)
                 if (u < warp) h = apply(run.run[u][lane], h);
             if (!failed) look_chunks(p, look, t.k, t.col);
             if (SPAN > kBlock && closes(p, t.k, kBlock)) {
                 __syncthreads();
-                if (warp == 0) publish_block(p, look, t, whole);
+                if (publishes) publish_block(p, look, t, whole);
             }
             if (!failed) look_blocks<SPAN>(p, look, t.k, t.col, p.start && live ? p.start + t.state + at.ch : nullptr);
             __syncthreads();
@@ -859,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) glr_bwd_kernel(const GlrPa
                 return false;
             }
             const float2 carry = look_carry<SPAN>(look, t.k);
-            if (warp == 0 && closes(p, t.k, SPAN)) publish_state<SPAN>(p, t, apply(whole, carry));
+            if (publishes && closes(p, t.k, SPAN)) publish_state<SPAN>(p, t, apply(whole, carry));
             const auto again = [&](int j, float2& x, float2& ig, float2& dy) {
                 const char* q = in + j * kCols * sizeof(IO);
                 ig = Pair<IO>::f(Pair<IO>::lds(q + kBoxBytes<IO>));
@@ -945,8 +946,21 @@ __global__ void __launch_bounds__(128) glr_step_kernel(int64_t B, int64_t D, int
     flag_nonfinite(status, acc);
 }
 
-thread_local int64_t g_fault_chunk1 = 0;
-thread_local unsigned long long g_fault_wait_ns = 0;
+// A missing carry armed for a thread's next call (the test hook): taken by that call, whatever becomes of it.
+struct WaitFault {
+    int64_t chunk1 = 0;
+    unsigned long long wait_ns = 0;
+};
+thread_local WaitFault g_fault;
+WaitFault take_fault() {
+    const WaitFault f = g_fault;
+    g_fault = WaitFault{};
+    return f;
+}
+void set_fault(GlrParams& p, const WaitFault& f) {
+    p.fault_chunk1 = f.chunk1;
+    if (f.wait_ns) p.wait_ns = f.wait_ns;
+}
 
 bool off16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
@@ -1088,17 +1102,13 @@ int64_t ssm_glr_ckpt_elems(int64_t B, int64_t L, int64_t D) {
 
 int ssm_glr_debug_arm_wait_fault(int64_t chunk, uint64_t wait_ns) {
     if (wait_ns > 10000000000ull) return SSM_ERR_INVALID_ARG;
-    ssm::g_fault_chunk1 = chunk < 0 ? 0 : chunk + 1;
-    ssm::g_fault_wait_ns = chunk < 0 ? 0 : wait_ns;
+    ssm::g_fault = chunk < 0 ? ssm::WaitFault{} : ssm::WaitFault{chunk + 1, wait_ns};
     return SSM_OK;
 }
 
 int ssm_glr_fwd(const ssm_glr_args* a, void* stream) {
     ssm::reset_launches();
-    const int64_t fault_chunk1 = ssm::g_fault_chunk1;  // an armed fault applies to this call only
-    const unsigned long long fault_wait_ns = ssm::g_fault_wait_ns;
-    ssm::g_fault_chunk1 = 0;
-    ssm::g_fault_wait_ns = 0;
+    const ssm::WaitFault fault = ssm::take_fault();
     int rc = ssm::check_seq(a);
     if (rc != SSM_OK) return rc;
     cudaStream_t s = (cudaStream_t)stream;
@@ -1106,8 +1116,7 @@ int ssm_glr_fwd(const ssm_glr_args* a, void* stream) {
     if (!a->y) return SSM_ERR_INVALID_ARG;
     ssm::GlrParams p = ssm::base_params(*a);
     p.start = a->h0; p.end = a->h_last; p.y = a->y;
-    p.fault_chunk1 = fault_chunk1;
-    if (fault_wait_ns) p.wait_ns = fault_wait_ns;
+    ssm::set_fault(p, fault);
     const size_t pub = ssm::glr_ws(a->B, a->L, a->D, ssm::chunk_tokens(a->io_dtype)).publish_bytes;
     return ssm::count_launches(a->io_dtype == SSM_BF16 ? ssm::launch_seq<__nv_bfloat16>(false, p, pub, s)
                                                        : ssm::launch_seq<float>(false, p, pub, s));
@@ -1115,6 +1124,7 @@ int ssm_glr_fwd(const ssm_glr_args* a, void* stream) {
 
 int ssm_glr_bwd(const ssm_glr_bwd_args* a, void* stream) {
     ssm::reset_launches();
+    const ssm::WaitFault fault = ssm::take_fault();
     if (!a) return SSM_ERR_INVALID_ARG;
     const ssm_glr_args& f = a->f;
     int rc = ssm::check_seq(&f);
@@ -1133,6 +1143,7 @@ int ssm_glr_bwd(const ssm_glr_bwd_args* a, void* stream) {
     ssm::GlrParams p = ssm::base_params(f);
     p.start = a->dh_last; p.end = a->dh0;
     p.dy = a->dy; p.dx = a->dx; p.dr = a->drgate; p.di = a->digate;
+    ssm::set_fault(p, fault);
     const size_t pub = ssm::glr_ws(f.B, f.L, f.D, ssm::chunk_tokens(f.io_dtype)).publish_bytes;
     rc = ssm::count_launches(f.io_dtype == SSM_BF16 ? ssm::launch_seq<__nv_bfloat16>(true, p, pub, s)
                                                     : ssm::launch_seq<float>(true, p, pub, s));
