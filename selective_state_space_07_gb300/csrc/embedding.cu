@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SRC src,
 }
 
 struct EmbedParams {
-    int n, V;
+    int V;
     int64_t D;
     float scale;
     const void* dy;
@@ -596,7 +596,7 @@ int ssm_embed_bwd(const ssm_embed_bwd_args* a, void* stream) {
     rc = ssm::count_launches(a->ids64 ? sort(int64_t{}) : sort(int32_t{}));
     if (rc != SSM_OK) return rc;
     ssm::EmbedParams p{};
-    p.n = (int)a->tokens; p.V = (int)a->V; p.D = a->D; p.scale = a->scale; p.dy = a->dy;
+    p.V = (int)a->V; p.D = a->D; p.scale = a->scale; p.dy = a->dy;
     p.off = off; p.order = order; p.sid = sid; p.dW = a->dW; p.part = reinterpret_cast<float*>(ws + w.part);
     p.pieces = (int)((a->tokens + ssm::kPiece - 1) / ssm::kPiece);
     // Vectors where rows and sums allow them: four elements in bf16, two in fp32 (16384 ids of 50001 x 1024 fp32: 70 us
