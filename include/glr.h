@@ -8,8 +8,9 @@
  *   log a_t = -c s r_t                                  (a_t in (0, 1])
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t,  y_t = h_t
  * h starts from h0 (zeros when NULL). sqrt(1 - a^2) keeps the state's
- * variance that of its input; it is evaluated as sqrt(-expm1(2 log a)), so
- * that it keeps its leading digits for decays near 1.
+ * variance that of its input; it is evaluated as sqrt(w (2 - w)) from
+ * w = 1 - a = -expm1(log a), so that it keeps its leading digits for decays
+ * near 1, and a from the exponential itself where it is small.
  * Backward for loss = <dy, y> + <dh_last, h_last>, with g_t the whole
  * gradient of h_t:
  *   g_t = dy_t + a_{t+1} g_{t+1}  (g_{L-1} = dy_{L-1} + dh_last)

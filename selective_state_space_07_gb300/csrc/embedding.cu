@@ -18,8 +18,8 @@
 // leaves their partial sums for a third kernel, which adds them in order.
 //
 // Measured, in percent of the HBM copy rate: the lookup of 16384 ids of
-// 50001 x 2048 bf16 17 us (rows named twice come from L2); its gradient 103 us
-// (67%): 11 the sort, 82 the rows (86% of the copy rate by themselves, most of
+// 50001 x 2048 bf16 21 us (79%; 16 when its rows are in L2 from the call
+// before), fp32 43 (77%); the gradient of the first 103 us (67%): 11 the sort, 82 the rows (86% of the copy rate by themselves, most of
 // them zeros written), the rest the joined sums. 64 ids of the same table:
 // 64 us (94%). Many tokens for narrow rows are bound by the sort: 65536 ids of
 // 50001 x 64 bf16 31 us (10%).
@@ -479,7 +479,7 @@ int launch_lookup(const ssm_embed_args& a, cudaStream_t s) {
                        a.D, a.scale, static_cast<const IO*>(a.W), static_cast<IO*>(a.out), blocks, static_cast<unsigned*>(a.status));
 }
 // Lanes and chunks by the row's width: at most 1024 columns a group in the
-// lookup (16384 of 50001 x 2048 bf16: 17.3 us; at most 512 18.9, 256 26.6);
+// lookup (16384 of 50001 x 2048 bf16, the same ids again: 17.3 us; at most 512 18.9, 256 26.6);
 // 256 in the gradient, whose sums then take few enough registers for 48 warps
 // an SM. Rows of up to 32 and 128 elements take 4 and 16 lanes (65536 of
 // 50001 x 32: 6.4 us, with a warp 12.6; the gradient 42.5 and 48.7).

@@ -15,7 +15,7 @@
 // where four of 16 take 105.)
 //
 // The state before a tile comes from the tiles before it in one pass over the
-// data: every tile publishes its map (P, H), and every 16th the state after
+// data (the published single-pass scan with look-back): every tile publishes its map (P, H), and every 16th the state after
 // it; a tile takes the last such state and applies the at most 15 maps in
 // between, in order. (Where few columns make the chain of those states count,
 // the state comes after every 256th tile, and the map of each block of 16,
@@ -33,8 +33,9 @@
 // The backward runs the same scheme from the last chunk to the first over
 // v = a g (what a token hands to the one before it): per warp (P, V), the
 // same products P. The states h_{t-1} that the gradients need are recomputed
-// in fp32 from the states that the forward saved every 32 tokens, so no bf16
-// copy of them enters the gradients.
+// in fp32 from the state that the forward saved before the tile's first token,
+// so no bf16 copy of them enters the gradients. (States are saved every 32
+// tokens for either type; a bf16 tile has 64 and takes every other one.)
 //
 // Measured, bf16 unless said, in percent of the HBM copy rate, for slow decays
 // (c softplus(lam) < 1/4): 4 x 4096 x 4096 forward with checkpoints 101 us

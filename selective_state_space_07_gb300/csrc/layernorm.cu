@@ -25,11 +25,11 @@
 // Column sums leave once a CTA: its groups add theirs in shared memory, in
 // group order, and a second kernel adds the CTAs', in CTA order.
 //
-// Measured, in percent of the HBM copy rate: 65536 x 2048 bf16 forward 97 us
-// (82%), backward 138 (86%); 16384 x 2048 25 (78%) and 41 (73%); 65537 x 1023
-// fp32 95 (83%) and 132 (90%), bf16 54 (74%) and 107 (56%: single elements,
-// instructions); 65536 x 512 29 (68%) and 43 (69%); 4096 x 16384 58 (69%) and
-// 97 (61%: one row an SM at a time), 2048 x 16384 fp32 59 (67%) and 98 (61%).
+// Measured, in percent of the HBM copy rate: 65536 x 2048 bf16 forward 95 us
+// (83%), backward 135 (88%); 16384 x 2048 24 (83%) and 39 (76%); 65537 x 1023
+// fp32 93 (86%) and 129 (92%), bf16 51 (77%) and 109 (55%: single elements,
+// instructions); 65536 x 512 33 (60%) and 41 (72%); 4096 x 16384 58 (69%) and
+// 98 (61%: one row an SM at a time), 2048 x 16384 fp32 59 (67%) and 98 (61%).
 // Wider rows are read from L2 again (4096 x 16384 bf16 that way: 153 and 214).
 #include <cmath>
 

@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const float* __restrict__ 
     flag_nonfinite(status, bad);
 }
 
-// One warp a group: scale and nibbles.
+// One warp a group: scale and nibbles. Done once for weights, and so left simple: a byte stored a lane bounds it (65536 x
+// 4096 with groups of 128 from bf16 340 us, 29% of the copy rate, from fp32 345; with groups of 32 993).
 template <typename IN>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(int64_t count, int group, const IN* __restrict__ w, uint8_t* q,
                                                         __nv_bfloat16* s) {
